@@ -1,0 +1,287 @@
+// The 8-bit cache: writing tokens, reading them back, and the norm and
+// rotation before a cache (include/tq.h has the contracts).
+//
+// All three move data: each is bound by HBM for long inputs and by launch
+// latency for a decode step's.
+#include "tq_q8.cuh"
+
+namespace tq {
+namespace {
+
+constexpr float kQ8Tiny = 7.888609052210118e-31f;   // 2^-100
+
+template <int FMT>
+__device__ __forceinline__ float q8_top() {
+  return FMT == TQ_Q8_INT8 ? 127.f : 448.f;
+}
+
+// ---- append ---------------------------------------------------------------
+// One CTA per (touched block, row x kv head, K or V).  A block that the call
+// completes is gathered (its old tokens from the ring, the others from the
+// input), reduced to its largest magnitude, and coded; a thread keeps its
+// share of the 64 x D values in registers, so each is read once.
+//
+// The 16-bit ring takes the new tokens of the newest two blocks.  A block
+// writes its own, with one exception: the first touched block reads its old
+// tokens from the ring half of its parity, so a later block of that parity
+// leaves its ring tokens to the first CTA, which writes them after its
+// reads.  So no CTA writes what another one reads.
+constexpr int kAppendThreads = 256;
+
+template <typename T, int FMT, int D>
+__global__ void __launch_bounds__(kAppendThreads) q8_append_kernel(const Q8AppendArgs a) {
+  constexpr int CH = D / 8;                              // 16-byte chunks per token
+  constexpr int ITEMS = kQ8Block * CH / kAppendThreads;  // chunks per thread
+  __shared__ unsigned red[kAppendThreads / 32];
+  const int unit = blockIdx.y, kv = blockIdx.z, tid = threadIdx.x;
+  const int b = unit / a.c.num_kv_heads, h = unit % a.c.num_kv_heads;
+  const int len = a.lens[b], fresh = a.n_rows ? a.n_rows[b] : a.n;
+  const bool invalid = len < 0 || fresh < 0 || fresh > a.n;
+  if (invalid || (int64_t)len + fresh > a.c.capacity) {
+    if (blockIdx.x == 0 && tid == 0) atomicOr(a.c.status, invalid ? kQ8StatusInvalid : kQ8StatusCapacity);
+    return;
+  }
+  if (fresh == 0) return;
+  const int end = len + fresh, first = len / kQ8Block, last = (end - 1) / kQ8Block;
+  const int blk = first + (int)blockIdx.x;
+  if (blk > last) return;
+  const uint4* in = reinterpret_cast<const uint4*>(
+      static_cast<const T*>(a.in[kv]) + b * a.row_stride[kv] + h * a.head_stride[kv]);
+  const int64_t tstride = a.token_stride[kv] / 8;
+  uint4* ring = reinterpret_cast<uint4*>(kv ? a.c.v_recent : a.c.k_recent) + (size_t)unit * kQ8Ring * CH;
+
+  if ((blk + 1) * kQ8Block <= end) {
+    uint4 x[ITEMS];
+    unsigned mx = 0;                                     // magnitudes' bits, two 16-bit lanes
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) {
+      const int i = tid + j * kAppendThreads, p = blk * kQ8Block + i / CH, c = i % CH;
+      x[j] = p < len ? ring[(p % kQ8Ring) * CH + c] : in[(int64_t)(p - len) * tstride + c];
+    }
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) {
+      const unsigned w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx = __vmaxu2(mx, w[e] & 0x7fff7fffu);
+    }
+    mx = max(mx & 0xffffu, mx >> 16);                    // bits of a magnitude order as magnitudes do,
+    mx = __reduce_max_sync(~0u, mx);                     // infinities and NaN above all numbers
+    if (tid % 32 == 0) red[tid / 32] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kAppendThreads / 32; ++w) mx = max(mx, red[w]);
+    const float amax = unpack16<T>(mx).x;
+    const bool bad = mx >= (Pair16<T>::kInf & 0xffffu), live = amax >= kQ8Tiny && !bad;
+    const float inv = live ? __fdiv_rn(q8_top<FMT>(), amax) : 0.f;
+    uint2* codes = reinterpret_cast<uint2*>(kv ? a.c.v_codes : a.c.k_codes) +
+                   ((size_t)unit * a.c.capacity + (size_t)blk * kQ8Block) * CH;
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) {
+      const unsigned w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+      unsigned o[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float2 lo = unpack16<T>(w[2 * e]), hi = unpack16<T>(w[2 * e + 1]);
+        if (!live) lo = hi = make_float2(0.f, 0.f);      // 0 * NaN would leave a NaN code
+        lo.x = __fmul_rn(lo.x, inv), lo.y = __fmul_rn(lo.y, inv);
+        hi.x = __fmul_rn(hi.x, inv), hi.y = __fmul_rn(hi.y, inv);
+        if (FMT == TQ_Q8_E4M3) {
+          o[e] = __nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3) |
+                 (unsigned)__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3) << 16;
+        } else {
+          // |y| <= 127 (1 + 2^-23): the low byte of y + 1.5 2^23, which the sum rounds to nearest even
+          const float m = 12582912.f;
+          const unsigned p0 = __byte_perm(__float_as_uint(lo.x + m), __float_as_uint(lo.y + m), 0x0040);
+          const unsigned p1 = __byte_perm(__float_as_uint(hi.x + m), __float_as_uint(hi.y + m), 0x0040);
+          o[e] = __byte_perm(p0, p1, 0x5410);
+        }
+      }
+      codes[tid + j * kAppendThreads] = make_uint2(o[0], o[1]);
+    }
+    if (tid == 0)
+      (kv ? a.c.v_scales : a.c.k_scales)[(size_t)unit * (a.c.capacity / kQ8Block) + blk] =
+          bad ? __uint_as_float(0x7fffffffu) : live ? __fdiv_rn(amax, q8_top<FMT>()) : 1.f;
+  }
+
+  auto to_ring = [&](int r) {
+    const int lo = max(r * kQ8Block, len), hi = min((r + 1) * kQ8Block, end);
+    for (int i = tid; i < (hi - lo) * CH; i += kAppendThreads) {
+      const int p = lo + i / CH;
+      ring[(p % kQ8Ring) * CH + i % CH] = in[(int64_t)(p - len) * tstride + i % CH];
+    }
+  };
+  if (blk >= last - 1 && (blk == first || ((blk - first) & 1))) to_ring(blk);
+  if (blk == first && last >= first + 2) {
+    __syncthreads();                                     // after this CTA's reads of the ring
+    to_ring(((last - first) & 1) ? last - 1 : last);
+  }
+}
+
+// ---- read -----------------------------------------------------------------
+constexpr int kReadThreads = 256;
+
+template <typename T, int FMT, int D>
+__global__ void __launch_bounds__(kReadThreads) q8_read_kernel(const Q8ReadArgs a) {
+  constexpr int CH = D / 8;
+  const int unit = blockIdx.y, kv = blockIdx.z, b = unit / a.c.num_kv_heads;
+  const int len = a.lens[b];
+  if (len < 0 || len > a.c.capacity) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.c.status, kQ8StatusInvalid);
+    return;
+  }
+  const int64_t i = (int64_t)blockIdx.x * kReadThreads + threadIdx.x;
+  const int64_t t = i / CH, p = a.start + t;
+  const int c = (int)(i % CH);
+  if (t >= a.n || p >= len) return;
+  uint4 r;
+  if (p >= len / kQ8Block * kQ8Block) {
+    r = reinterpret_cast<const uint4*>(kv ? a.c.v_recent : a.c.k_recent)[((size_t)unit * kQ8Ring + p % kQ8Ring) * CH + c];
+  } else {
+    const float s = (kv ? a.c.v_scales : a.c.k_scales)[(size_t)unit * (a.c.capacity / kQ8Block) + p / kQ8Block];
+    const uint2 w = reinterpret_cast<const uint2*>(kv ? a.c.v_codes : a.c.k_codes)[((size_t)unit * a.c.capacity + p) * CH + c];
+    unsigned o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = unpack16<__half>(codes_to_half2<FMT>(((e & 2) ? w.y : w.x) >> (16 * (e & 1))));
+      o[e] = pack16<T>(__fmul_rn(f.x, s), __fmul_rn(f.y, s));
+    }
+    r = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  reinterpret_cast<uint4*>(a.out[kv])[((size_t)unit * a.n + t) * CH + c] = r;
+}
+
+// ---- norm and rotation ------------------------------------------------------
+// One CTA per token: its angles' cosines and sines once (float64 reduction of
+// position x frequency to a turn, then a float32 sincos), then D / 16 lanes
+// per head, each with one 16-byte chunk of either half of the head, so that
+// both elements of every pair are in one lane in either layout of the pairs.
+constexpr int kRopeThreads = 256;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const NormRopeArgs a) {
+  constexpr int L = D / 16;                              // lanes per head
+  __shared__ float2 cs[D / 2];
+  const int64_t tok = blockIdx.x;
+  const int b = (int)(tok / a.n), t = (int)(tok % a.n), tid = threadIdx.x;
+  if (tid < D / 2) {
+    const double two_pi = 6.283185307179586476925286766559;
+    const double ang = (double)a.positions[tok] * (double)a.inv_freq[tid];
+    const float r = (float)(ang - two_pi * rint(ang / two_pi));
+    float s, c;
+    sincosf(r, &s, &c);
+    cs[tid] = make_float2(c, s);
+  }
+  __syncthreads();
+  const int lane = tid % L;
+  for (int h0 = 0; h0 < a.Hq + a.Hkv; h0 += kRopeThreads / L) {
+    const int h = h0 + tid / L;
+    const bool on = h < a.Hq + a.Hkv, isq = h < a.Hq;
+    if (!on) break;                                      // whole groups of L lanes leave together
+    const int hh = isq ? h : h - a.Hq;
+    const T* src = isq ? static_cast<const T*>(a.q) + b * a.q_row + t * a.q_token + hh * a.q_head
+                       : static_cast<const T*>(a.k) + b * a.k_row + t * a.k_token + hh * a.k_head;
+    const void* wt = isq ? a.q_weight : a.k_weight;
+    float x[16];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint4 v = reinterpret_cast<const uint4*>(src)[lane + e * L];
+      const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack16<T>(w[i]);
+        x[8 * e + 2 * i] = f.x, x[8 * e + 2 * i + 1] = f.y;
+      }
+    }
+    if (wt) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
+      const unsigned mask = ((1u << L) - 1u) << (tid % 32 / L * L);
+#pragma unroll
+      for (int o = L / 2; o; o /= 2) ss += __shfl_xor_sync(mask, ss, o);
+      float r = 1.0f / sqrtf(ss / D + a.eps);
+      // bf16 squares can leave float32 at either end: such heads take float64
+      double rd = 0.0;
+      const bool wide = Pair16<T>::kWide && !(ss > 1e-30f && ss < 1e38f);
+      if (wide) {
+        double sd = 0.0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sd += (double)x[i] * x[i];
+#pragma unroll
+        for (int o = L / 2; o; o /= 2) sd += __shfl_xor_sync(mask, sd, o);
+        rd = 1.0 / sqrt(sd / D + a.eps);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint4 v = reinterpret_cast<const uint4*>(wt)[lane + e * L];
+        const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = unpack16<T>(w[i]);
+          float &x0 = x[8 * e + 2 * i], &x1 = x[8 * e + 2 * i + 1];
+          x0 = wide ? (float)(x0 * rd * f.x) : x0 * (r * f.x);
+          x1 = wide ? (float)(x1 * rd * f.y) : x1 * (r * f.y);
+        }
+      }
+    }
+    float y[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int i0 = a.interleaved ? 2 * i : i, i1 = a.interleaved ? 2 * i + 1 : i + 8;
+      const int j = a.interleaved ? (i < 4 ? 4 * lane + i : D / 4 + 4 * lane + i - 4) : 8 * lane + i;
+      const float2 w = cs[j];
+      y[i0] = x[i0] * w.x - x[i1] * w.y;
+      y[i1] = x[i1] * w.x + x[i0] * w.y;
+    }
+    T* dst = isq ? static_cast<T*>(a.q_out) + ((size_t)tok * a.Hq + hh) * D
+                 : static_cast<T*>(a.k_out) + (((size_t)b * a.Hkv + hh) * a.n + t) * D;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      reinterpret_cast<uint4*>(dst)[lane + e * L] =
+          make_uint4(pack16<T>(y[8 * e], y[8 * e + 1]), pack16<T>(y[8 * e + 2], y[8 * e + 3]),
+                     pack16<T>(y[8 * e + 4], y[8 * e + 5]), pack16<T>(y[8 * e + 6], y[8 * e + 7]));
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_q8_append(const Q8AppendArgs& a, cudaStream_t s) {
+  const dim3 grid((unsigned)((a.n + kQ8Block - 2) / kQ8Block + 1), (unsigned)(a.c.batch * a.c.num_kv_heads), 2);
+  auto go = [&](auto fn) { fn<<<grid, kAppendThreads, 0, s>>>(a); };
+  const bool h = a.c.dtype == TQ_DTYPE_FP16, i8 = a.c.format == TQ_Q8_INT8;
+#define TQ_APPEND(D)                                                                            \
+  h ? (i8 ? go(q8_append_kernel<__half, TQ_Q8_INT8, D>) : go(q8_append_kernel<__half, TQ_Q8_E4M3, D>)) \
+    : (i8 ? go(q8_append_kernel<__nv_bfloat16, TQ_Q8_INT8, D>) : go(q8_append_kernel<__nv_bfloat16, TQ_Q8_E4M3, D>))
+  if (a.c.head_dim == 64) TQ_APPEND(64);
+  else TQ_APPEND(128);
+#undef TQ_APPEND
+  return cudaGetLastError();
+}
+
+cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s) {
+  const int64_t chunks = (int64_t)a.n * (a.c.head_dim / 8);
+  const dim3 grid((unsigned)((chunks + kReadThreads - 1) / kReadThreads), (unsigned)(a.c.batch * a.c.num_kv_heads), 2);
+  auto go = [&](auto fn) { fn<<<grid, kReadThreads, 0, s>>>(a); };
+  const bool h = a.c.dtype == TQ_DTYPE_FP16, i8 = a.c.format == TQ_Q8_INT8;
+#define TQ_READ(D)                                                                              \
+  h ? (i8 ? go(q8_read_kernel<__half, TQ_Q8_INT8, D>) : go(q8_read_kernel<__half, TQ_Q8_E4M3, D>)) \
+    : (i8 ? go(q8_read_kernel<__nv_bfloat16, TQ_Q8_INT8, D>) : go(q8_read_kernel<__nv_bfloat16, TQ_Q8_E4M3, D>))
+  if (a.c.head_dim == 64) TQ_READ(64);
+  else TQ_READ(128);
+#undef TQ_READ
+  return cudaGetLastError();
+}
+
+cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t s) {
+  const unsigned grid = (unsigned)((int64_t)a.batch * a.n);
+  const bool h = a.dtype == TQ_DTYPE_FP16;
+  if (a.d == 64)
+    h ? norm_rope_kernel<__half, 64><<<grid, kRopeThreads, 0, s>>>(a)
+      : norm_rope_kernel<__nv_bfloat16, 64><<<grid, kRopeThreads, 0, s>>>(a);
+  else
+    h ? norm_rope_kernel<__half, 128><<<grid, kRopeThreads, 0, s>>>(a)
+      : norm_rope_kernel<__nv_bfloat16, 128><<<grid, kRopeThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace tq

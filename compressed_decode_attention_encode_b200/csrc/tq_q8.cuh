@@ -1,0 +1,138 @@
+// Internal declarations of the 8-bit cache (tq_q8_*) and of the norm and
+// rotation before a cache: argument blocks and launchers.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "../../include/tq.h"
+
+namespace tq {
+
+constexpr int kQ8Block = 64;        // tokens that share a scale
+constexpr int kQ8Ring = 128;        // slots of the 16-bit ring: two blocks
+constexpr int kQ8MaxRows = 1024;
+constexpr int kQ8MaxQueries = 64;
+constexpr int kQ8MaxGroup = 16;
+
+// Status word bits of a tq_q8_cache.
+constexpr int kQ8StatusInvalid = 1;
+constexpr int kQ8StatusCapacity = 2;
+
+struct Q8AppendArgs {
+  tq_q8_cache c;
+  const void* in[2];                 // K, V
+  int64_t row_stride[2], head_stride[2], token_stride[2];
+  int n;
+  const int32_t* lens;
+  const int32_t* n_rows;
+};
+
+struct Q8ReadArgs {
+  tq_q8_cache c;
+  const int32_t* lens;
+  int64_t start;
+  int n;
+  void* out[2];
+};
+
+struct Q8AttendArgs {
+  tq_q8_cache c;
+  const void* q;
+  int64_t row_stride, token_stride, head_stride;
+  int Hq, G, n;
+  const int32_t* lens;
+  const int32_t* n_rows;
+  float scale_log2;                  // sigma * log2(e)
+  void* out;
+  uint8_t* scratch;
+};
+
+struct NormRopeArgs {
+  int batch, n, Hq, Hkv, d, dtype;
+  const void* q;
+  const void* k;
+  int64_t q_row, q_token, q_head, k_row, k_token, k_head;
+  const int32_t* positions;
+  const float* inv_freq;
+  const void* q_weight;
+  const void* k_weight;
+  float eps;
+  int interleaved;
+  void* q_out;
+  void* k_out;
+};
+
+cudaError_t launch_q8_append(const Q8AppendArgs& a, cudaStream_t s);
+cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s);
+size_t q8_attend_scratch(const tq_q8_cache& c, int Hq, int n, int num_sms);
+cudaError_t launch_q8_attend(const Q8AttendArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t s);
+
+#ifdef __CUDACC__
+// ---- 16-bit values and codes in registers --------------------------------
+template <typename T>
+struct Pair16;                       // the packed pair of a 16-bit type
+template <>
+struct Pair16<__half> {
+  using type = __half2;
+  static constexpr uint32_t kInf = 0x7c007c00u;
+  static constexpr bool kWide = false;   // whether squares of values can leave float32
+};
+template <>
+struct Pair16<__nv_bfloat16> {
+  using type = __nv_bfloat162;
+  static constexpr uint32_t kInf = 0x7f807f80u;
+  static constexpr bool kWide = true;
+};
+
+template <typename T>
+__device__ __forceinline__ float2 unpack16(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack16<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <>
+__device__ __forceinline__ float2 unpack16<__nv_bfloat16>(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack16(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack16<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Two codes (the low 16 bits of w) as fp16, which holds every code exactly.
+template <int FMT>
+__device__ __forceinline__ uint32_t codes_to_half2(uint32_t w) {
+  if (FMT == TQ_Q8_E4M3) {
+    uint32_t r;
+    asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, lo; }" : "=r"(r) : "r"(w));
+    return r;
+  }
+  // 0x6400 | u is 1024 + u for a byte u; u = code + 128
+  const uint32_t u = __byte_perm(w ^ 0x8080u, 0x64646464u, 0x4140);
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6480)));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Whether a 16-bit pair holds a NaN or an infinity.
+template <typename T>
+__device__ __forceinline__ bool pair_bad(uint32_t w) {
+  constexpr uint32_t inf = Pair16<T>::kInf;
+  return (w & inf & 0xffffu) == (inf & 0xffffu) || (w & inf & 0xffff0000u) == (inf & 0xffff0000u);
+}
+#endif
+
+}  // namespace tq

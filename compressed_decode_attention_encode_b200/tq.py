@@ -42,6 +42,13 @@ class tq_vec_config(Structure):
                 ("seed", c_uint64)]
 
 
+class tq_q8_cache(Structure):
+    _fields_ = [("batch", c_int32), ("num_kv_heads", c_int32), ("head_dim", c_int32), ("format", c_int32),
+                ("dtype", c_int32), ("capacity", c_int64), ("k_codes", c_void_p), ("v_codes", c_void_p),
+                ("k_scales", c_void_p), ("v_scales", c_void_p), ("k_recent", c_void_p),
+                ("v_recent", c_void_p), ("status", c_void_p)]
+
+
 _lib = None
 
 # (name, restype, argtypes) of every exported symbol
@@ -85,6 +92,16 @@ SIGNATURES = [
     ("tq_vec_get_status", c_int32, [c_void_p, c_void_p]),
     ("tq_export_vectors", c_int32, [c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_void_p,
                                     c_void_p, c_void_p, c_void_p]),
+    ("tq_q8_append", c_int32, [c_void_p, c_void_p, c_void_p, *[c_int64] * 6, c_int32, c_void_p, c_void_p,
+                               c_void_p]),
+    ("tq_q8_read", c_int32, [c_void_p, c_void_p, c_int64, c_int32, c_void_p, c_void_p, c_void_p]),
+    ("tq_q8_attention_bytes", c_int32, [c_void_p, c_int32, c_int32, POINTER(c_size_t)]),
+    ("tq_q8_attention", c_int32, [c_void_p, c_void_p, c_int64, c_int64, c_int64, c_int32, c_int32, c_void_p,
+                                  c_void_p, c_float, c_void_p, c_void_p, c_size_t, c_void_p]),
+    ("tq_q8_get_status", c_int32, [c_void_p, c_void_p]),
+    ("tq_qk_norm_rope", c_int32, [*[c_int32] * 6, c_void_p, c_int64, c_int64, c_int64, c_void_p, c_int64,
+                                  c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_float, c_int32,
+                                  c_void_p, c_void_p, c_void_p]),
     ("tq_rotation_signs", c_int32, [c_uint64, c_int32, POINTER(c_int8)]),
     ("tq_qjl_matrix", c_int32, [c_uint64, c_int32, c_int32, POINTER(c_float)]),
 ]
@@ -484,3 +501,229 @@ class TQVecIndex:
                                        p["bits"], p["s16"], p["rn16"], _stream_handle(stream)),
                "tq_export_vectors")
         return out
+
+
+# ---- 8-bit cache ------------------------------------------------------------
+
+Q8_BLOCK = 64        # tokens that share a scale
+Q8_RING = 128        # slots of the 16-bit ring
+
+
+def _q8_dtypes():
+    import torch
+    return {torch.float16: 0, torch.bfloat16: 1}
+
+
+class TQ8Cache:
+    """A layer's KV cache in 8 bits: whole blocks of 64 tokens as int8 or e4m3
+    codes with one float32 scale per (row, kv head, block), the open block in a
+    16-bit ring.  Every method is a direct call into libtq.so.
+
+    The object keeps no lengths: each call takes ``lens``, an int32 tensor [B]
+    on the cache's device, which the caller advances once per step for all
+    layers, so that calls can be captured in CUDA graphs.
+
+    ``buffers``: tensors of an earlier cache to take over, by the names
+    ``k_codes``, ``v_codes`` [B, Hkv, capacity, d] (int8 or float8_e4m3fn),
+    ``k_scales``, ``v_scales`` [B, Hkv, capacity / 64] (float32), ``k_recent``,
+    ``v_recent`` [B, Hkv, 128, d] (``dtype``)."""
+
+    FORMATS = {"int8": 0, "e4m3": 1}
+
+    def __init__(self, batch, num_kv_heads, head_dim, capacity, format="int8", dtype=None,
+                 device="cuda", buffers=None):
+        import torch
+        dtype = torch.float16 if dtype is None else dtype
+        if format not in self.FORMATS:
+            raise ValueError("format is 'int8' or 'e4m3'")
+        if dtype not in _q8_dtypes():
+            raise ValueError("dtype is torch.float16 or torch.bfloat16")
+        device = torch.device(device)
+        if device.type == "cuda" and device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        self.device, self.dtype = device, dtype
+        code = torch.int8 if format == "int8" else torch.float8_e4m3fn
+        shape = (batch, num_kv_heads)
+        for kv in "kv":
+            for name, more, dt in (("codes", (capacity, head_dim), code),
+                                   ("scales", (capacity // Q8_BLOCK,), torch.float32),
+                                   ("recent", (Q8_RING, head_dim), dtype)):
+                t = buffers[f"{kv}_{name}"] if buffers is not None else None
+                if t is None:
+                    t = torch.empty(shape + more, dtype=dt, device=device)
+                elif tuple(t.shape) != shape + more or t.dtype != dt or t.device != device or not t.is_contiguous():
+                    raise ValueError(f"{kv}_{name}: expected a contiguous {dt} {list(shape + more)} on {device}")
+                setattr(self, f"{kv}_{name}", t)
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self.struct = tq_q8_cache(batch, num_kv_heads, head_dim, self.FORMATS[format], _q8_dtypes()[dtype],
+                                  capacity, _ptr(self.k_codes), _ptr(self.v_codes), _ptr(self.k_scales),
+                                  _ptr(self.v_scales), _ptr(self.k_recent), _ptr(self.v_recent),
+                                  _ptr(self.status))
+        self._ref = ctypes.addressof(self.struct)
+        self._scratch_bytes = {}
+        self._shape = (batch, num_kv_heads, head_dim)
+        # the sizes are checked here once, by the library (no device call)
+        _check(lib().tq_q8_append(self._ref, None, None, 0, 0, 0, 0, 0, 0, 0, None, None, None), "TQ8Cache")
+
+    def _guard(self):
+        """The cache's device as the current one (the library launches there)."""
+        import torch
+        return torch.cuda.device(self.device)
+
+    def _stream(self, stream):
+        import torch
+        if stream is None:
+            return torch.cuda.current_stream(self.device).cuda_stream
+        if stream.device != self.device:
+            raise ValueError(f"expected a stream of {self.device}")
+        return stream.cuda_stream
+
+    def _ints(self, t, what):
+        import torch
+        if t is None:
+            return None
+        if t.dtype != torch.int32 or t.device != self.device or t.dim() != 1 or t.shape[0] != self._shape[0] \
+                or not t.is_contiguous():
+            raise ValueError(f"{what}: expected a contiguous int32 [{self._shape[0]}] on {self.device}")
+        return t.data_ptr()
+
+    def _values(self, t, what, dims):
+        if t.dtype != self.dtype or t.device != self.device or t.dim() != dims:
+            raise ValueError(f"{what}: expected {self.dtype} with {dims} dimensions on {self.device}")
+        if t.stride(-1) != 1:
+            raise ValueError(f"{what}: the head dimension must be contiguous")
+        return t.data_ptr()
+
+    def append(self, k, v, lens, n_rows=None, stream=None):
+        """k, v [B, Hkv, n, d] (any strides with d contiguous) become tokens
+        lens[b] .. lens[b] + n_rows[b] - 1 of row b (n_rows None: n each)."""
+        b, h, d = self._shape
+        n = k.shape[2] if k.dim() == 4 else -1
+        if tuple(k.shape) != (b, h, n, d) or k.shape != v.shape:
+            raise ValueError(f"k, v: expected [{b}, {h}, n, {d}]")
+        kp, vp = self._values(k, "k", 4), self._values(v, "v", 4)
+        ks, vs = k.stride(), v.stride()
+        lp, rp = self._ints(lens, "lens"), self._ints(n_rows, "n_rows")
+        with self._guard():
+            code = lib().tq_q8_append(self._ref, kp, vp, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], n, lp, rp,
+                                      self._stream(stream))
+        _check(code, "tq_q8_append")
+
+    def read(self, lens, start=0, n=None, out=None, stream=None):
+        """Positions start .. start + n - 1 of every row as 16-bit K, V
+        [B, Hkv, n, d].  ``out``: a pair to write into, whose values that belong
+        to no token stay; without it they are zero."""
+        import torch
+        b, h, d = self._shape
+        if out is None:
+            if n is None:
+                raise ValueError("read needs n or out")
+            out = tuple(torch.zeros((b, h, n, d), dtype=self.dtype, device=self.device) for _ in "kv")
+        ko, vo = out
+        n = ko.shape[2] if n is None and ko.dim() == 4 else n
+        for t in out:
+            if tuple(t.shape) != (b, h, n, d) or t.dtype != self.dtype or t.device != self.device \
+                    or not t.is_contiguous():
+                raise ValueError(f"out: expected two contiguous {self.dtype} [{b}, {h}, {n}, {d}] on {self.device}")
+        lp = self._ints(lens, "lens")
+        with self._guard():
+            code = lib().tq_q8_read(self._ref, lp, start, n, ko.data_ptr(), vo.data_ptr(), self._stream(stream))
+        _check(code, "tq_q8_read")
+        return out
+
+    def scratch_bytes(self, num_q_heads, n):
+        """Bytes of scratch of an attention call (as tq_q8_attention_bytes)."""
+        key = (num_q_heads, n)
+        if key not in self._scratch_bytes:
+            size = c_size_t()
+            with self._guard():
+                code = lib().tq_q8_attention_bytes(self._ref, num_q_heads, n, ctypes.byref(size))
+            _check(code, "tq_q8_attention_bytes")
+            self._scratch_bytes[key] = size.value
+        return self._scratch_bytes[key]
+
+    def attention(self, q, lens, n_rows=None, out=None, softmax_scale=0.0, scratch=None, stream=None):
+        """q [B, n, Hq, d] (or [B, Hq, d] for one token): the newest n tokens'
+        queries, attending to their row's positions up to their own; lens
+        counts them.  Returns ``out`` in q's shape and type.  ``scratch``: a
+        uint8 tensor of scratch_bytes; without it one is taken from PyTorch's
+        allocator for the call."""
+        import torch
+        b, h, d = self._shape
+        one = q.dim() == 3
+        n = 1 if one else q.shape[1]
+        hq = q.shape[-2]
+        qp = self._values(q, "q", 3 if one else 4)
+        if q.shape[0] != b or q.shape[-1] != d:
+            raise ValueError(f"q: expected [{b}, n, Hq, {d}]")
+        qs = q.stride()
+        lp, rp = self._ints(lens, "lens"), self._ints(n_rows, "n_rows")
+        size = self.scratch_bytes(hq, n)
+        if stream is not None and (out is None or scratch is None):
+            # what is allocated here belongs to the stream of the call
+            with torch.cuda.stream(stream):
+                return self.attention(q, lens, n_rows, out, softmax_scale, scratch)
+        if out is None:
+            out = torch.empty(q.shape, dtype=self.dtype, device=self.device)
+        elif out.shape != q.shape or out.dtype != self.dtype or out.device != self.device or not out.is_contiguous():
+            raise ValueError("out: expected a contiguous tensor of q's shape and type")
+        if scratch is None:
+            scratch = torch.empty(size, dtype=torch.uint8, device=self.device)
+        elif scratch.dtype != torch.uint8 or scratch.device != self.device or not scratch.is_contiguous():
+            raise ValueError(f"scratch: expected a contiguous uint8 tensor on {self.device}")
+        with self._guard():
+            code = lib().tq_q8_attention(self._ref, qp, qs[0], 0 if one else qs[1], qs[-2], hq, n, lp, rp,
+                                         softmax_scale, out.data_ptr(), scratch.data_ptr(), scratch.numel(),
+                                         self._stream(stream))
+        _check(code, "tq_q8_attention")
+        return out
+
+    def get_status(self, stream=None):
+        """Latched device status (0 = TQ_OK); waits for the stream, then clears it."""
+        with self._guard():
+            return lib().tq_q8_get_status(self._ref, self._stream(stream))
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                 q_out=None, k_out=None, stream=None):
+    """Norm of every query and key head and rotation by position (see
+    tq_qk_norm_rope): q [B, n, Hq, d], k [B, n, Hkv, d] (any strides with d
+    contiguous, e.g. slices of a packed projection), positions int32 [B, n],
+    inv_freq float32 [d / 2].  Returns q_out [B, n, Hq, d] and k_out
+    [B, Hkv, n, d], the layouts that the caches' calls take."""
+    import torch
+    if q.dim() != 4 or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
+        raise ValueError("expected q [B, n, Hq, d] and k [B, n, Hkv, d]")
+    b, n, hq, d = q.shape
+    hk, dev, dtype = k.shape[2], q.device, q.dtype
+    if dtype not in _q8_dtypes() or k.dtype != dtype or not q.is_cuda or k.device != dev:
+        raise ValueError("q, k: expected CUDA float16 or bfloat16 tensors of one type and device")
+    if (d > 1 and q.numel() and q.stride(3) != 1) or (d > 1 and k.numel() and k.stride(3) != 1):
+        raise ValueError("q, k: the head dimension must be contiguous")
+    for t, what, shape, dt in ((positions, "positions", (b, n), torch.int32), (inv_freq, "inv_freq", (d // 2,), torch.float32),
+                               (q_weight, "q_weight", (d,), dtype), (k_weight, "k_weight", (d,), dtype),
+                               (q_out, "q_out", (b, n, hq, d), dtype), (k_out, "k_out", (b, hk, n, d), dtype)):
+        if t is None:
+            if what in ("positions", "inv_freq"):
+                raise ValueError(f"{what} is needed")
+        elif tuple(t.shape) != shape or t.dtype != dt or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{what}: expected a contiguous {dt} {list(shape)} on {dev}")
+    if stream is not None and (q_out is None or k_out is None):
+        with torch.cuda.stream(stream):
+            return qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, q_out, k_out)
+    if q_out is None:
+        q_out = torch.empty((b, n, hq, d), dtype=dtype, device=dev)
+    if k_out is None:
+        k_out = torch.empty((b, hk, n, d), dtype=dtype, device=dev)
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"expected a stream of {dev}")
+    s = (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
+    qs, ks = q.stride(), k.stride()
+    with torch.cuda.device(dev):
+        code = lib().tq_qk_norm_rope(b, n, hq, hk, d, _q8_dtypes()[dtype], q.data_ptr(), qs[0], qs[1], qs[2],
+                                     k.data_ptr(), ks[0], ks[1], ks[2], positions.data_ptr(), inv_freq.data_ptr(),
+                                     None if q_weight is None else q_weight.data_ptr(),
+                                     None if k_weight is None else k_weight.data_ptr(), eps, int(interleaved),
+                                     q_out.data_ptr(), k_out.data_ptr(), s)
+    _check(code, "tq_qk_norm_rope")
+    return q_out, k_out

@@ -429,6 +429,150 @@ tq_status tq_export_vectors(tq_vec_index* index, const void* codes, int64_t star
                             int64_t count, uint8_t* codes_out, uint8_t* bits_out,
                             uint16_t* s16_out, uint16_t* rn16_out, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * A KV cache in 8 bits.
+ * The plain counterpart of the compressed cold store, for callers who want
+ * most of the memory saved and none of the estimator's error: every whole
+ * block of 64 tokens is held in 8 bits with one float32 scale per (row, kv
+ * head, block) for K and one for V.  It has no host-side state: lengths are
+ * device arrays that the caller advances, so every call can be captured in
+ * a CUDA graph and replayed as the rows grow, and the layers of a model
+ * share one array.
+ *
+ * What is held.  Position p of a row belongs to block p / 64.  Of a row of
+ * length L, the tokens of its floor(L / 64) whole blocks are read from the
+ * codes, and the L % 64 tokens of its open block from a 16-bit ring, where
+ * position p has slot p % 128.  The ring also keeps the newest whole block's
+ * tokens, so a row's length may be set back by up to 64 tokens of what was
+ * appended last (rejected drafts): appending again from there gives the same
+ * codes as if the rejected tokens had never been written.
+ *
+ * Quantisation of a block (64 x d values x, K and V apart), all in float32
+ * with M = 127 (int8) or 448 (e4m3), each operation rounded to nearest even:
+ *   a = max |x|,  scale = a / M,  code = round(x * (M / a))
+ *   a < 2^-100:          scale = 1, codes 0 (only bf16 holds such values)
+ *   a not finite:        scale = NaN, codes 0: the block reads as NaN
+ * A token is rounded once, whatever the calls that brought it.
+ * ---------------------------------------------------------------------- */
+#define TQ_Q8_INT8 0          /* codes: two's complement, -127..127           */
+#define TQ_Q8_E4M3 1          /* codes: 8-bit floating point, 4 exponent bits */
+#define TQ_DTYPE_FP16 0
+#define TQ_DTYPE_BF16 1
+
+typedef struct tq_q8_cache {
+  int32_t batch;            /* rows B, 1..1024                               */
+  int32_t num_kv_heads;     /* Hkv >= 1                                      */
+  int32_t head_dim;         /* d: 64 or 128                                  */
+  int32_t format;           /* TQ_Q8_INT8 or TQ_Q8_E4M3                      */
+  int32_t dtype;            /* of inputs, outputs and ring: TQ_DTYPE_*       */
+  int64_t capacity;         /* tokens per row: a multiple of 64, < 2^31 - 64 */
+  void* k_codes;            /* device [B, Hkv, capacity, d], one byte each   */
+  void* v_codes;
+  float* k_scales;          /* device [B, Hkv, capacity / 64]                */
+  float* v_scales;
+  void* k_recent;           /* device [B, Hkv, 128, d], 16 bits each         */
+  void* v_recent;
+  int32_t* status;          /* device word, zero at first (tq_q8_get_status) */
+} tq_q8_cache;
+
+/*
+ * Write new tokens.
+ *   k, v    device 16-bit [B, Hkv, n, d] by strides, in elements, of the
+ *           row, the head and the token (d contiguous); strides are
+ *           non-negative multiples of 8, addresses multiples of 16 bytes
+ *   n       tokens a row at most, >= 0 (0 is a no-op)
+ *   lens    device int32 [B]: tokens that row b holds before the call; the
+ *           call leaves it as it is
+ *   n_rows  device int32 [B], 0 <= n_rows[b] <= n: row b appends its first
+ *           n_rows[b] tokens; NULL: n for every row
+ * A row whose length is negative, or whose n_rows is out of range, is left
+ * as it was and TQ_ERR_INVALID_ARG is latched in the status word; a row
+ * that would exceed the capacity likewise, with TQ_ERR_CAPACITY.
+ */
+tq_status tq_q8_append(const tq_q8_cache* cache, const void* k, const void* v,
+                       int64_t k_row_stride, int64_t k_head_stride, int64_t k_token_stride,
+                       int64_t v_row_stride, int64_t v_head_stride, int64_t v_token_stride,
+                       int32_t n, const int32_t* lens, const int32_t* n_rows, cudaStream_t stream);
+
+/*
+ * Read positions start .. start + n - 1 of every row back to 16 bits.
+ *   lens          device int32 [B]: tokens that row b holds
+ *   k_out, v_out  device 16-bit [B, Hkv, n, d], contiguous, 16-byte aligned;
+ *                 what belongs to no token of a row is left as it was
+ * A value is code * scale in float32, rounded once; the open block's values
+ * are the appended ones.  Lengths below 0 or above the capacity are latched
+ * as TQ_ERR_INVALID_ARG and their rows left as they were.
+ */
+tq_status tq_q8_read(const tq_q8_cache* cache, const int32_t* lens, int64_t start, int32_t n,
+                     void* k_out, void* v_out, cudaStream_t stream);
+
+/* Bytes of scratch that tq_q8_attention needs for a cache (its sizes only:
+ * the pointers may be NULL) on the current device. */
+tq_status tq_q8_attention_bytes(const tq_q8_cache* cache, int32_t num_q_heads, int32_t n,
+                                size_t* bytes);
+
+/*
+ * Attention of the newest n tokens of every row over the row's cache.
+ *   q        device 16-bit [B, n, Hq, d] by strides of the row, the token
+ *            and the head (as for tq_q8_append); Hq a multiple of Hkv with
+ *            Hq / Hkv <= 16, 1 <= n <= 64
+ *   lens     device int32 [B]: tokens that row b holds, the n newest (those
+ *            of q) among them
+ *   n_rows   device int32 [B] or NULL: row b has n_rows[b] <= n queries; what
+ *            out holds behind them is left as it was
+ *   out      device 16-bit [B, n, Hq, d], contiguous, 16-byte aligned
+ *   softmax_scale  sigma; 0 selects 1/sqrt(d)
+ *   scratch  device, 256-byte aligned, at least tq_q8_attention_bytes; it
+ *            holds nothing between calls, and calls whose GPU work overlaps
+ *            need one each
+ * Query i of row b attends to its positions below lens[b] - n_rows[b] + 1 + i:
+ *   out = sum_p softmax_p(sigma <q, k_p>) v_p
+ * and is zero where there is none.  Sums and softmax statistics are float32;
+ * the products take fp16 operands, which hold codes and fp16 values exactly.
+ * A token that holds a NaN or an infinity, or whose block does, makes the
+ * outputs NaN that attend to it and no others.  Lengths and n_rows out of
+ * range are latched as TQ_ERR_INVALID_ARG, and the row's outputs are NaN.
+ */
+tq_status tq_q8_attention(const tq_q8_cache* cache, const void* q, int64_t row_stride,
+                          int64_t token_stride, int64_t head_stride, int32_t num_q_heads,
+                          int32_t n, const int32_t* lens, const int32_t* n_rows,
+                          float softmax_scale, void* out, void* scratch, size_t scratch_bytes,
+                          cudaStream_t stream);
+
+/* Synchronize `stream`, then return and clear the latched status: TQ_OK,
+ * TQ_ERR_CAPACITY or TQ_ERR_INVALID_ARG. */
+tq_status tq_q8_get_status(const tq_q8_cache* cache, cudaStream_t stream);
+
+/*
+ * Norm of every query and key head and rotation by position, in one pass:
+ * the step before a cache (K is cached after any positional encoding), from
+ * a model's projections, token by token, to the layouts that the caches
+ * take.  For a head x [d] at position p:
+ *   y = x / sqrt(mean(x^2) + eps) * weight       (weight NULL: y = x)
+ *   pair j of y is turned by the angle p * inv_freq[j], j < d / 2
+ * in float32 (angles in float64), rounded once.
+ *   q       device 16-bit [B, n, Hq, d], by strides of row, token and head
+ *   k       device 16-bit [B, n, Hkv, d], likewise
+ *           (d contiguous; strides non-negative multiples of 8, addresses
+ *           multiples of 16 bytes; d = 64 or 128)
+ *   positions   device int32 [B, n]
+ *   inv_freq    device float32 [d / 2]
+ *   q_weight, k_weight  device 16-bit [d], 16-byte aligned, or NULL
+ *   interleaved 0: pair j is (y_j, y_{j + d/2}); 1: (y_2j, y_{2j+1})
+ *   q_out   device 16-bit [B, n, Hq, d], contiguous, 16-byte aligned
+ *   k_out   device 16-bit [B, Hkv, n, d], likewise (what tq_encode_append,
+ *           tq_evict_window and tq_q8_append take)
+ * Outputs must not overlap inputs.  num_q_heads or num_kv_heads may be 0
+ * (its pointers are then not used).
+ */
+tq_status tq_qk_norm_rope(int32_t batch, int32_t n, int32_t num_q_heads, int32_t num_kv_heads,
+                          int32_t head_dim, int32_t dtype, const void* q, int64_t q_row_stride,
+                          int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                          int64_t k_row_stride, int64_t k_token_stride, int64_t k_head_stride,
+                          const int32_t* positions, const float* inv_freq, const void* q_weight,
+                          const void* k_weight, float eps, int32_t interleaved, void* q_out,
+                          void* k_out, cudaStream_t stream);
+
 /*
  * Measurement hook: when `start` and `stop` are non-NULL, every following
  * tq_decode_attention call on this handle records `start` on its stream
