@@ -119,13 +119,13 @@ def attention_bound(o, w, q, ck, sk, cv, sv, sigma, dtype):
             + 2.0 ** -25 * ref * np.abs(cv).sum(0) + 2.0 ** -25)
 
 
-def check_attention(st, q, out, rows=None, sigma=0.0, before=None):
+def check_attention(st, q, out, rows=None, sigma=0.0, before=None, only=None):
     b, h, d = st.shape
     n, hq = q.shape[1], q.shape[2]
     g = hq // h
     got, qd = out.double().cpu().numpy(), q.double().cpu().numpy()
     sig = sigma or 1 / math.sqrt(d)
-    for i in range(b):
+    for i in range(b) if only is None else only:
         r = n if rows is None else rows[i]
         for u in range(h):
             heads = slice(u * g, (u + 1) * g)
@@ -363,13 +363,14 @@ def test_attention_refuses_rows_on_the_device():
     st = Stream(4, 1, 64, 128, "int8", "fp16")
     st.append(32, 100, [100, 10, 20, 30])
     q = values(33, (4, 2, 4, 64), "fp16", False).cuda()
-    good = st.c.attention(q, st.lens())
     for lens, rows, bad in (([100, -1, 20, 30], [2, 2, 2, 2], 1), ([100, 10, 129, 30], [2, 2, 2, 2], 2),
                             ([100, 10, 20, 30], [2, 2, 2, 3], 3), ([100, 10, 20, 30], [-1, 2, 2, 2], 0)):
         out = st.c.attention(q, torch.tensor(lens, **INT), torch.tensor(rows, **INT))
         assert st.c.get_status() == 1 and st.c.get_status() == 0
-        for i in range(4):
-            assert torch.isnan(out[i]).all() if i == bad else torch.equal(out[i], good[i])
+        assert torch.isnan(out[bad]).all()
+        # the other rows' tiles are split over the card by the lengths that are valid: another order of
+        # the same sums, which the bound holds for
+        check_attention(st, q, out, only=[i for i in range(4) if i != bad])
 
 
 def test_attention_query_strides_streams_and_repeats():
