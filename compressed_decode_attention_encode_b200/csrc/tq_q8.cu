@@ -139,11 +139,13 @@ __global__ void __launch_bounds__(kReadThreads) q8_read_kernel(const Q8ReadArgs 
   } else {
     const float s = (kv ? a.c.v_scales : a.c.k_scales)[(size_t)unit * (a.c.capacity / kQ8Block) + p / kQ8Block];
     const uint2 w = reinterpret_cast<const uint2*>(kv ? a.c.v_codes : a.c.k_codes)[((size_t)unit * a.c.capacity + p) * CH + c];
-    unsigned o[4];
+    unsigned f[4], o[4];
+    codes_to_half4<FMT>(w.x, f[0], f[1]);
+    codes_to_half4<FMT>(w.y, f[2], f[3]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float2 f = unpack16<__half>(codes_to_half2<FMT>(((e & 2) ? w.y : w.x) >> (16 * (e & 1))));
-      o[e] = pack16<T>(__fmul_rn(f.x, s), __fmul_rn(f.y, s));
+      const float2 v = unpack16<__half>(f[e]);
+      o[e] = pack16<T>(__fmul_rn(v.x, s), __fmul_rn(v.y, s));
     }
     r = make_uint4(o[0], o[1], o[2], o[3]);
   }

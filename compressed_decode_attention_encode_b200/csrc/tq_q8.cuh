@@ -113,18 +113,22 @@ __device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Two codes (the low 16 bits of w) as fp16, which holds every code exactly.
+// Four codes as fp16, which holds every code exactly: the low two, the high two.
 template <int FMT>
-__device__ __forceinline__ uint32_t codes_to_half2(uint32_t w) {
+__device__ __forceinline__ void codes_to_half4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if (FMT == TQ_Q8_E4M3) {
-    uint32_t r;
-    asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, lo; }" : "=r"(r) : "r"(w));
-    return r;
+    asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
+        : "=r"(lo), "=r"(hi) : "r"(w));
+  } else {
+    // 0x6400 | u is 1024 + u for a byte u; u = code + 128
+    const __half2 bias = __half2half2(__ushort_as_half(0x6480));
+    w ^= 0x80808080u;
+    const uint32_t l = __byte_perm(w, 0x64646464u, 0x4140), h = __byte_perm(w, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&l), bias);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&h), bias);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
   }
-  // 0x6400 | u is 1024 + u for a byte u; u = code + 128
-  const uint32_t u = __byte_perm(w ^ 0x8080u, 0x64646464u, 0x4140);
-  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6480)));
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // Whether a 16-bit pair holds a NaN or an infinity.

@@ -10,9 +10,11 @@
 // The work is the batch's tiles (a unit's whole blocks of 64 tokens, then its
 // open block), flattened and cut into equal runs, one per CTA, so that rows of
 // any length share the card; every CTA finds its run from the lengths alone
-// (they are device memory).  A unit inside one CTA's run is finished there;
-// the others leave partial results that a second kernel joins in a fixed
-// order.
+// (they are device memory).  Each unit has kUnitCost places before its first
+// tile, which stand for what a pass costs besides its tiles (its queries'
+// latency, the open block's, the join of the warps).  A unit inside one CTA's
+// run is finished there; the others leave partial results that a second
+// kernel joins in a fixed order.
 #include <cmath>
 
 #include "tq_q8.cuh"
@@ -22,9 +24,10 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kStages = 3;
-constexpr int kMinTiles = 2;                 // tiles that a CTA takes at least
+constexpr int kUnitCost = 3;                 // of a unit besides its tiles, in tiles
+constexpr int kMinTiles = 4;                 // places that a CTA takes at least
 constexpr float kLowest = -3.0e38f;          // of a reference before its first token
-constexpr float kShift = 7.f;                // numerator weights are 2^7 at their reference,
+constexpr float kShift = 7.f;                // numerator weights are 2^7 at their reference (mv holds it less 7),
 constexpr float kLazy = 8.f;                 // and a reference moves when one exceeds it by 2^8: below fp16's 2^16
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -88,17 +91,18 @@ __device__ __forceinline__ float lds32f(uint32_t a) {
 __device__ __forceinline__ bool row_valid(const Q8AttendArgs& a, int len, int nr) {
   return len >= 0 && len <= a.c.capacity && nr >= 0 && nr <= a.n;
 }
-__device__ __forceinline__ int row_tiles(const Q8AttendArgs& a, int b) {
+// Places of a unit of row b.
+__device__ __forceinline__ int row_places(const Q8AttendArgs& a, int b) {
   const int len = a.lens[b], nr = a.n_rows ? a.n_rows[b] : a.n;
-  return row_valid(a, len, nr) && nr > 0 ? len / kQ8Block + (len % kQ8Block != 0) : 0;
+  return row_valid(a, len, nr) && nr > 0 && len > 0 ? kUnitCost + len / kQ8Block + (len % kQ8Block != 0) : 0;
 }
-// Tiles before each row into pre[0 .. batch] (a unit's tiles x units of a row).
+// Places before each row into pre[0 .. batch] (a unit's places x units of a row).
 __device__ __forceinline__ void plan_rows(const Q8AttendArgs& a, int subs, uint32_t* pre, uint32_t* warp_sums) {
   uint32_t total = 0;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   for (int b0 = 0; b0 < a.c.batch; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
-    const uint32_t v = b < a.c.batch ? (uint32_t)row_tiles(a, b) * subs : 0;
+    const uint32_t v = b < a.c.batch ? (uint32_t)row_places(a, b) * subs : 0;
     uint32_t s = v;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
@@ -126,40 +130,51 @@ __device__ __forceinline__ uint32_t plan_ctas(uint32_t tiles, uint32_t grid) {
 __device__ __forceinline__ uint32_t cta_start(uint32_t c, uint32_t tiles, uint32_t ctas) {
   return (uint32_t)((uint64_t)c * tiles / ctas);
 }
-// The CTA whose run holds tile t.
+// The CTA whose run holds place t.
 __device__ __forceinline__ uint32_t cta_of(uint32_t t, uint32_t tiles, uint32_t ctas) {
   return (uint32_t)((((uint64_t)t + 1) * ctas + tiles - 1) / tiles) - 1;
 }
 
-// A place in the flattened tiles: row, unit of the row (kv head x query group), tile of the unit.
-struct Cursor {
-  int row, sub, tile, tiles, whole;
-  __device__ void load(const Q8AttendArgs& a) {
+// A CTA's run, segment by segment: a segment is the run's tiles [begin, end) of one unit (kv head x query
+// group of a row), never empty.
+struct Walk {
+  int row, sub;
+  uint32_t left;                           // places of the run behind this segment
+  int whole, tiles, begin, end;            // of the unit: whole blocks, tiles; of the segment: tiles
+  __device__ void enter(const Q8AttendArgs& a, uint32_t pos) {
     const int len = a.lens[row];
     whole = len / kQ8Block;
     tiles = whole + (len % kQ8Block != 0);
+    const uint32_t take = min(left, (uint32_t)(kUnitCost + tiles) - pos);
+    begin = max((int)pos - kUnitCost, 0);
+    end = (int)(pos + take) - kUnitCost;
+    left -= take;
   }
-  __device__ void seek(const Q8AttendArgs& a, const uint32_t* pre, uint32_t s) {
-    int lo = 0, hi = a.c.batch;              // pre[lo] <= s < pre[hi]
+  // To the next segment; false at the end of the run.
+  __device__ bool next(const Q8AttendArgs& a, const uint32_t* pre, int subs) {
+    do {
+      if (left == 0) return false;
+      if (++sub == subs) {
+        sub = 0;
+        do ++row;
+        while (pre[row + 1] == pre[row]);
+      }
+      enter(a, 0);
+    } while (end <= begin);
+    return true;
+  }
+  __device__ bool first(const Q8AttendArgs& a, const uint32_t* pre, int subs, uint32_t t0, uint32_t t1) {
+    int lo = 0, hi = a.c.batch;            // pre[lo] <= t0 < pre[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
-      (pre[mid] <= s ? lo : hi) = mid;
+      (pre[mid] <= t0 ? lo : hi) = mid;
     }
     row = lo;
-    load(a);
-    const uint32_t off = s - pre[row];
-    sub = off / tiles;
-    tile = off % tiles;
-  }
-  // To the next tile; the caller knows that there is one.
-  __device__ void next(const Q8AttendArgs& a, const uint32_t* pre, int subs) {
-    if (++tile < tiles) return;
-    tile = 0;
-    if (++sub < subs) return;
-    sub = 0;
-    do ++row;
-    while (pre[row + 1] == pre[row]);
-    load(a);
+    const uint32_t off = t0 - pre[row], places = (pre[row + 1] - pre[row]) / subs;
+    sub = off / places;
+    left = t1 - t0;
+    enter(a, off % places);
+    return end > begin || next(a, pre, subs);
   }
 };
 
@@ -277,7 +292,7 @@ struct Pass {
   __device__ __forceinline__ void weights(const float (&s)[NT][4], const float (&f)[NT][2], float lsv, int first,
                                           uint32_t bad, float (&w)[NT][4]) {
     float pl[NT][4];
-    bool move = false;
+    float top_l = kLowest, top_v = kLowest;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -286,9 +301,9 @@ struct Pass {
         pl[t][e] = fmaf(s[t][e], f[t][j], -ml[t][j]);
         w[t][e] = fmaf(s[t][e], f[t][j], lsv - mv[t][j]);
         const bool vis = !VIS || first + gid + 8 * (e >> 1) < end[t][j];
-        move |= vis && (pl[t][e] > kLazy || w[t][e] > kLazy);
+        if (vis) top_l = fmaxf(top_l, pl[t][e]), top_v = fmaxf(top_v, w[t][e]);
       }
-    if (__any_sync(~0u, move)) {
+    if (__any_sync(~0u, top_l > kLazy || top_v > kLazy + kShift)) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -301,7 +316,7 @@ struct Pass {
           float mx = fmaxf(x0, x1);
 #pragma unroll
           for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
-          const float nl = fmaxf(ml[t][j], mx), nv = mx > kLowest ? fmaxf(mv[t][j], mx + lsv) : mv[t][j];
+          const float nl = fmaxf(ml[t][j], mx), nv = mx > kLowest ? fmaxf(mv[t][j], mx + lsv - kShift) : mv[t][j];
           l[t][j] *= ex2(ml[t][j] - nl);
           const float c = ex2(mv[t][j] - nv);
           ml[t][j] = nl;
@@ -321,7 +336,7 @@ struct Pass {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float p = ex2(pl[t][e]);
-        w[t][e] = ex2(w[t][e] + kShift);
+        w[t][e] = ex2(w[t][e]);
         if (VIS) {
           const bool vis = first + gid + 8 * (e >> 1) < end[t][e & 1];
           const bool nan = bad >> (gid + 8 * (e >> 1)) & 1;
@@ -348,8 +363,9 @@ struct Pass {
       const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const uint32_t a0 = codes_to_half2<FMT>(wa[x]), a1 = codes_to_half2<FMT>(wb[x]);
-        const uint32_t a2 = codes_to_half2<FMT>(wa[x] >> 16), a3 = codes_to_half2<FMT>(wb[x] >> 16);
+        uint32_t a0, a1, a2, a3;
+        codes_to_half4<FMT>(wa[x], a0, a2);
+        codes_to_half4<FMT>(wb[x], a1, a3);
 #pragma unroll
         for (int t = 0; t < NT; ++t) mma16816(s[t], a0, a1, a2, a3, qf[t][4 * j + x][0], qf[t][4 * j + x][1], __half());
       }
@@ -382,8 +398,9 @@ struct Pass {
       for (int y = 0; y < 2; ++y) {
         const uint32_t lo = __byte_perm(v[0][x], v[1][x], y ? 0x7362 : 0x5140);
         const uint32_t hi = __byte_perm(v[2][x], v[3][x], y ? 0x7362 : 0x5140);
-        const uint32_t a0 = codes_to_half2<FMT>(lo), a1 = codes_to_half2<FMT>(lo >> 16);
-        const uint32_t a2 = codes_to_half2<FMT>(hi), a3 = codes_to_half2<FMT>(hi >> 16);
+        uint32_t a0, a1, a2, a3;
+        codes_to_half4<FMT>(lo, a0, a1);
+        codes_to_half4<FMT>(hi, a2, a3);
 #pragma unroll
         for (int t = 0; t < NT; ++t) mma16816(o[2 * x + y][t], a0, a1, a2, a3, b[t][0], b[t][1], __half());
       }
@@ -416,16 +433,6 @@ struct Pass {
           k[i][4 * j + 2 * x + 1][0] = w.z, k[i][4 * j + 2 * x + 1][1] = w.w;
           if (pair_bad<T>(w.x) || pair_bad<T>(w.y) || pair_bad<T>(w.z) || pair_bad<T>(w.w)) bad |= 1u << (gid + 8 * i);
         }
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      uint32_t raw[KS][2];
-      float unused = 0.f;
-      if (Pair16<T>::kWide) load_q<false>(a, row, kvh, r0, t, raw, unused);
-#pragma unroll
-      for (int x = 0; x < KS; ++x)
-        mma16816(s[t], k[0][x][0], k[1][x][0], k[0][x][1], k[1][x][1], Pair16<T>::kWide ? raw[x][0] : qf[t][x][0],
-                 Pair16<T>::kWide ? raw[x][1] : qf[t][x][1], T());
-    }
     uint32_t v[4][KS];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -436,6 +443,16 @@ struct Pass {
         v[i][4 * x] = w.x, v[i][4 * x + 1] = w.y, v[i][4 * x + 2] = w.z, v[i][4 * x + 3] = w.w;
         if (pair_bad<T>(w.x) || pair_bad<T>(w.y) || pair_bad<T>(w.z) || pair_bad<T>(w.w)) bad |= 1u << r;
       }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      uint32_t raw[KS][2];
+      float unused = 0.f;
+      if (Pair16<T>::kWide) load_q<false>(a, row, kvh, r0, t, raw, unused);
+#pragma unroll
+      for (int x = 0; x < KS; ++x)
+        mma16816(s[t], k[0][x][0], k[1][x][0], k[0][x][1], k[1][x][1], Pair16<T>::kWide ? raw[x][0] : qf[t][x][0],
+                 Pair16<T>::kWide ? raw[x][1] : qf[t][x][1], T());
     }
     bad = __reduce_or_sync(~0u, bad);
     if (bad) {                                             // 0 x NaN would reach queries that do not see the token
@@ -535,9 +552,8 @@ struct Pass {
   }
 };
 
-template <typename T>
 __device__ __forceinline__ float result(float o, float ml, float mv, float l) {
-  return l == 0.f ? 0.f : o * (ex2(mv - ml - kShift) / l);
+  return l == 0.f ? 0.f : o * (ex2(mv - ml) / l);
 }
 
 template <typename T, int FMT, int D, int NT>
@@ -562,132 +578,193 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q8_attend_kernel
   ps.lane = threadIdx.x % 32, ps.warp = threadIdx.x / 32;
   ps.gid = ps.lane / 4, ps.tig = ps.lane % 4;
   const uint32_t ring = smem_u32(smem) + ps.warp * kStages * S::STAGE;
-  Cursor get, use;
-  use.seek(a, pre, t0);
-  get = use;
-  uint32_t left = t1 - t0;                                 // tiles still to fetch
-  // The warp's 16 tokens of the next tile into a stage; open blocks are read where they are used.
-  auto fetch = [&](int stage) {
-    if (left > 0) {
-      if (get.tile < get.whole) {
-        const size_t unit = (size_t)get.row * a.c.num_kv_heads + get.sub / groups;
-        const size_t at = (unit * a.c.capacity + (size_t)get.tile * kQ8Block + 16 * ps.warp) * D;
-        const uint8_t* kp = static_cast<const uint8_t*>(a.c.k_codes) + at;
-        const uint8_t* vp = static_cast<const uint8_t*>(a.c.v_codes) + at;
-        const uint32_t st = ring + stage * S::STAGE;
+  // The warp's 16 tokens of the run's next whole block go to a stage of the warp's ring (open blocks are
+  // read where they are used): 16-byte copies from kp, vp, and the two scales.
+  Walk get;
+  const uint8_t *kp = nullptr, *vp = nullptr;
+  const float* sp = nullptr;
+  int more = 0;                                            // whole blocks to fetch from kp, vp on
+  auto aim = [&](bool on) {
+    for (; on; on = get.next(a, pre, subs)) {
+      more = min(get.end, get.whole) - get.begin;
+      if (more <= 0) continue;
+      const size_t unit = (size_t)get.row * a.c.num_kv_heads + get.sub / groups;
+      const size_t at = (unit * a.c.capacity + (size_t)get.begin * kQ8Block + 16 * ps.warp) * D + 16 * ps.lane;
+      kp = static_cast<const uint8_t*>(a.c.k_codes) + at;
+      vp = static_cast<const uint8_t*>(a.c.v_codes) + at;
+      sp = (ps.lane ? a.c.v_scales : a.c.k_scales) + unit * (a.c.capacity / kQ8Block) + get.begin;
+      return;
+    }
+    more = 0;
+  };
+  uint32_t dst[S::SLAB / 512];
 #pragma unroll
-        for (int i = 0; i < S::SLAB / 512; ++i) {
-          const int x = i * 32 + ps.lane, r = x / (D / 16), c = x % (D / 16), d = slab_at<D>(r, c);
-          cp_async16(st + d, kp + 16 * x);
-          cp_async16(st + S::SLAB + d, vp + 16 * x);
-        }
-        if (ps.lane < 2)
-          cp_async4(st + 2 * S::SLAB + 4 * ps.lane,
-                    (ps.lane ? a.c.v_scales : a.c.k_scales) + unit * (a.c.capacity / kQ8Block) + get.tile);
+  for (int i = 0; i < S::SLAB / 512; ++i) {
+    const int x = i * 32 + ps.lane;
+    dst[i] = slab_at<D>(x / (D / 16), x % (D / 16));
+  }
+  auto fetch = [&](uint32_t st) {
+    if (more > 0) {
+#pragma unroll
+      for (int i = 0; i < S::SLAB / 512; ++i) {
+        cp_async16(st + dst[i], kp + 512 * i);
+        cp_async16(st + S::SLAB + dst[i], vp + 512 * i);
       }
-      if (--left > 0) get.next(a, pre, subs);
+      if (ps.lane < 2) cp_async4(st + 2 * S::SLAB + 4 * ps.lane, sp);
+      kp += kQ8Block * D, vp += kQ8Block * D, ++sp;
+      if (--more == 0) aim(get.next(a, pre, subs));
     }
     cp_commit();
   };
+  Walk use;
+  bool on = use.first(a, pre, subs, t0, t1);
+  get = use;
+  aim(on);
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) fetch(i);
+  for (int i = 0; i < kStages - 1; ++i) fetch(ring + i * S::STAGE);
 
-  bool fresh = true;                                       // the next tile begins a unit's pass
-  uint32_t seg = t0;                                       // its first tile
-  int stage = 0;
-  for (uint32_t t = t0; t < t1; ++t) {
-    fetch(stage == 0 ? kStages - 1 : stage - 1);
+  uint32_t st = ring, ahead = ring + (kStages - 1) * S::STAGE;
+  for (; on; on = use.next(a, pre, subs)) {
     const int kvh = use.sub / groups, r0 = use.sub % groups * S::ROWS;
-    if (fresh) ps.start(a, use.row, kvh, r0), seg = t, fresh = false;
-    cp_wait<kStages - 1>();
-    __syncwarp();
-    if (use.tile < use.whole) {
-      const uint32_t st = ring + stage * S::STAGE;
-      const int first = use.tile * kQ8Block + 16 * ps.warp;
-      if ((use.tile + 1) * kQ8Block <= ps.min_end) ps.template codes<false>(st, first);
+    ps.start(a, use.row, kvh, r0);
+    const int blocks = min(use.end, use.whole);
+    for (int tile = use.begin; tile < blocks; ++tile) {
+      fetch(ahead);
+      cp_wait<kStages - 1>();
+      __syncwarp();
+      const int first = tile * kQ8Block + 16 * ps.warp;
+      if ((tile + 1) * kQ8Block <= ps.min_end) ps.template codes<false>(st, first);
       else ps.template codes<true>(st, first);
-    } else {
-      ps.open(a, use.row, kvh, r0, use.whole);
+      __syncwarp();                                        // every lane has read before the stage is filled again
+      ahead = st;
+      st = st == ring + (kStages - 1) * S::STAGE ? ring : st + S::STAGE;
     }
-    __syncwarp();
-    stage = stage + 1 == kStages ? 0 : stage + 1;
-    if (use.tile + 1 == use.tiles || t + 1 == t1) {        // the end of the unit, or of the run
-      ps.join(area, stats);
-      const bool whole_unit = use.tile + 1 == use.tiles && t - seg + 1 == (uint32_t)use.tiles;
-      if (ps.warp == 0) {
-        float* part = reinterpret_cast<float*>(a.scratch) + ((size_t)blockIdx.x * 2 + (seg != t0)) * S::ROWS * S::OROW;
-        const int nr = a.n_rows ? a.n_rows[use.row] : a.n;
+    if (use.end > use.whole) ps.open(a, use.row, kvh, r0, use.whole);
+    ps.join(area, stats);
+    if (ps.warp == 0) {
+      const bool all = use.begin == 0 && use.end == use.tiles;
+      // its second result where the unit begins inside the run: of two units that the run shares, one does
+      const uint32_t unit0 = pre[use.row] + (uint32_t)use.sub * (kUnitCost + use.tiles) + kUnitCost;
+      float* part = reinterpret_cast<float*>(a.scratch) + ((size_t)blockIdx.x * 2 + (t0 < unit0)) * S::ROWS * S::OROW;
+      const int nr = a.n_rows ? a.n_rows[use.row] : a.n;
 #pragma unroll
-        for (int q = 0; q < NT; ++q)
+      for (int q = 0; q < NT; ++q)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int r = 8 * q + 2 * ps.tig + j, i = (r0 + r) / a.G, h = (r0 + r) % a.G;
-            if (i >= nr) continue;
-            if (whole_unit) {
-              T* out = static_cast<T*>(a.out) + (((size_t)use.row * a.n + i) * a.Hq + kvh * a.G + h) * D + D / 8 * ps.gid;
+        for (int j = 0; j < 2; ++j) {
+          const int r = 8 * q + 2 * ps.tig + j, i = (r0 + r) / a.G, h = (r0 + r) % a.G;
+          if (i >= nr) continue;
+          if (all) {
+            T* out = static_cast<T*>(a.out) + (((size_t)use.row * a.n + i) * a.Hq + kvh * a.G + h) * D + D / 8 * ps.gid;
 #pragma unroll
-              for (int m = 0; m < D / 16; ++m)
-                reinterpret_cast<uint32_t*>(out)[m] =
-                    pack16<T>(result<T>(ps.o[m][q][j], ps.ml[q][j], ps.mv[q][j], ps.l[q][j]),
-                              result<T>(ps.o[m][q][j + 2], ps.ml[q][j], ps.mv[q][j], ps.l[q][j]));
-            } else {
-              float* p = part + r * S::OROW;
+            for (int m = 0; m < D / 16; ++m)
+              reinterpret_cast<uint32_t*>(out)[m] =
+                  pack16<T>(result(ps.o[m][q][j], ps.ml[q][j], ps.mv[q][j], ps.l[q][j]),
+                            result(ps.o[m][q][j + 2], ps.ml[q][j], ps.mv[q][j], ps.l[q][j]));
+          } else {
+            float* p = part + r * S::OROW;
 #pragma unroll
-              for (int m = 0; m < D / 16; ++m)
-                *reinterpret_cast<float2*>(p + D / 8 * ps.gid + 2 * m) = make_float2(ps.o[m][q][j], ps.o[m][q][j + 2]);
-              if (ps.gid == 0) *reinterpret_cast<float4*>(p + D) = make_float4(ps.ml[q][j], ps.mv[q][j], ps.l[q][j], 0.f);
-            }
+            for (int m = 0; m < D / 16; ++m)
+              *reinterpret_cast<float2*>(p + D / 8 * ps.gid + 2 * m) = make_float2(ps.o[m][q][j], ps.o[m][q][j + 2]);
+            if (ps.gid == 0) *reinterpret_cast<float4*>(p + D) = make_float4(ps.ml[q][j], ps.mv[q][j], ps.l[q][j], 0.f);
           }
-      }
-      fresh = true;
+        }
     }
-    if (t + 1 < t1) use.next(a, pre, subs);
   }
 }
 
 // Joins the partial results of units that several CTAs share, one block per
 // (unit, query row), and writes what no CTA had work for: zeros for rows
-// without tokens, NaN for rows whose length is refused.
+// without tokens, NaN for rows whose length is refused.  It is bound by the
+// latency of its loads: the warps take the results in turn, a warp 32 of them
+// at a time, each lane first one result's references and sum, then all lanes
+// D / 32 dims of every result, the loads of eight together.
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kThreads) q8_join_kernel(const Q8AttendArgs a, uint32_t grid) {
   using S = Shape<D, NT>;
+  constexpr int E = D / 32;
   extern __shared__ uint32_t pre[];
   __shared__ uint32_t sums[kWarps];
+  __shared__ float wm[kWarps][3], wo[kWarps][D];
   const int R = a.n * a.G, groups = (R + S::ROWS - 1) / S::ROWS, subs = a.c.num_kv_heads * groups;
   const int row = blockIdx.y, kvh = blockIdx.x / R, r = blockIdx.x % R, i = r / a.G;
   plan_rows(a, subs, pre, sums);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int len = a.lens[row], nr = a.n_rows ? a.n_rows[row] : a.n;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const bool valid = row_valid(a, len, nr);
   if (valid && i >= nr) return;
-  const int d = threadIdx.x;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   T* out = static_cast<T*>(a.out) + (((size_t)row * a.n + i) * a.Hq + kvh * a.G + r % a.G) * D;
-  const int units = valid ? len / kQ8Block + (len % kQ8Block != 0) : 0;
-  if (units == 0) {
-    if (d < D) out[d] = valid ? (T)0.f : (T)__uint_as_float(0x7fffffffu);
+  if (!valid || len == 0) {
+    if (threadIdx.x < D) out[threadIdx.x] = valid ? (T)0.f : (T)__uint_as_float(0x7fffffffu);
     return;
   }
-  const uint32_t tiles = pre[a.c.batch], ctas = plan_ctas(tiles, grid);
-  const uint32_t first = pre[row] + (uint32_t)(kvh * groups + r / S::ROWS) * units, last = first + units - 1;
-  const uint32_t c0 = cta_of(first, tiles, ctas), c1 = cta_of(last, tiles, ctas);
-  if (c0 == c1 || d >= D) return;
+  const uint32_t places = pre[a.c.batch], ctas = plan_ctas(places, grid), unit = (pre[row + 1] - pre[row]) / subs;
+  const uint32_t first = pre[row] + (uint32_t)(kvh * groups + r / S::ROWS) * unit + kUnitCost;
+  const uint32_t c0 = cta_of(first, places, ctas), c1 = cta_of(first + unit - kUnitCost - 1, places, ctas);
+  if (c0 == c1) return;
+  // CTA c's first result, or its second where the unit begins inside its run
+  const uint32_t slot0 = cta_start(c0, places, ctas) < first;
   const float* part = reinterpret_cast<const float*>(a.scratch) + (size_t)(r % S::ROWS) * S::OROW;
-  // CTA c's result: its first one, or its second where its run begins before the unit
-  auto at = [&](uint32_t c) {
-    const uint32_t slot = c == c0 && cta_start(c, tiles, ctas) < first;
-    return part + (size_t)(c * 2 + slot) * S::ROWS * S::OROW;
-  };
-  float gl = kLowest, gv = kLowest, sum = 0.f, o = 0.f;
-  for (uint32_t c = c0; c <= c1; ++c) {
-    const float* p = at(c);
-    gl = fmaxf(gl, p[D]), gv = fmaxf(gv, p[D + 1]);
+  float gl = kLowest, gv = kLowest, sum = 0.f, o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  for (uint32_t b = c0 + warp; b <= c1; b += 32 * kWarps) {
+    const uint32_t c = b + kWarps * lane;                  // this lane's CTA
+    const int n = (int)min(32u, (c1 - b) / kWarps + 1);
+    float ml = kLowest, mv = kLowest, l = 0.f;
+    if (lane < n) {
+      const float4 x = *reinterpret_cast<const float4*>(part + (size_t)(c * 2 + (c == c0 ? slot0 : 0)) * S::ROWS * S::OROW + D);
+      ml = x.x, mv = x.y, l = x.z;
+    }
+    float nl = fmaxf(gl, ml), nv = fmaxf(gv, mv);
+#pragma unroll
+    for (int d = 16; d; d /= 2) nl = fmaxf(nl, __shfl_xor_sync(~0u, nl, d)), nv = fmaxf(nv, __shfl_xor_sync(~0u, nv, d));
+    l *= ex2(ml - nl);
+#pragma unroll
+    for (int d = 16; d; d /= 2) l += __shfl_xor_sync(~0u, l, d);
+    sum = sum * ex2(gl - nl) + l;
+    const float keep = ex2(gv - nv), w = ex2(mv - nv);
+    gl = nl, gv = nv;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= keep;
+    for (int x0 = 0; x0 < n; x0 += 8) {
+      float p[8][E];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const uint32_t cx = min(b + kWarps * (x0 + x), c1 - (c1 - b) % kWarps);
+        const float* src = part + (size_t)(cx * 2 + (cx == c0 ? slot0 : 0)) * S::ROWS * S::OROW + E * lane;
+        if (E == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          p[x][0] = v.x, p[x][1] = v.y, p[x][E - 2] = v.z, p[x][E - 1] = v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          p[x][0] = v.x, p[x][1] = v.y;
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const float wx = __shfl_sync(~0u, w, x0 + x);
+        if (x0 + x < n)
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = fmaf(wx, p[x][e], o[e]);
+      }
+    }
   }
-  for (uint32_t c = c0; c <= c1; ++c) {
-    const float* p = at(c);
-    sum += p[D + 2] * ex2(p[D] - gl);
-    o += p[d] * ex2(p[D + 1] - gv);
+  if (lane == 0) wm[warp][0] = gl, wm[warp][1] = gv, wm[warp][2] = sum;
+#pragma unroll
+  for (int e = 0; e < E; ++e) wo[warp][E * lane + e] = o[e];
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  gl = gv = kLowest, sum = 0.f;
+  float t = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) gl = fmaxf(gl, wm[w][0]), gv = fmaxf(gv, wm[w][1]);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    sum += wm[w][2] * ex2(wm[w][0] - gl);
+    t += wo[w][threadIdx.x] * ex2(wm[w][1] - gv);
   }
-  out[d] = (T)result<T>(o, gl, gv, sum);
+  out[threadIdx.x] = (T)result(t, gl, gv, sum);
 }
 
 // Query rows of one pass: 8 where a unit has no more, else 16.
@@ -695,7 +772,8 @@ int pick_nt(int rows) { return rows <= 8 ? 1 : 2; }
 
 uint32_t grid_of(const tq_q8_cache& c, int Hq, int n, int num_sms) {
   const int rows = n * (Hq / c.num_kv_heads), nt = pick_nt(rows);
-  const int64_t tiles = (int64_t)c.batch * c.num_kv_heads * ((rows + 8 * nt - 1) / (8 * nt)) * (c.capacity / kQ8Block);
+  const int64_t tiles = (int64_t)c.batch * c.num_kv_heads * ((rows + 8 * nt - 1) / (8 * nt)) *
+                        (c.capacity / kQ8Block + kUnitCost);
   const int64_t most = (int64_t)num_sms * ctas_per_sm(c.head_dim, nt), want = (tiles + kMinTiles - 1) / kMinTiles;
   return (uint32_t)(want < most ? want : most);
 }
