@@ -25,7 +25,7 @@ namespace {
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kStages = 3;
 constexpr int kUnitCost = 3;                 // of a unit besides its tiles, in tiles
-constexpr int kMinTiles = 4;                 // places that a CTA takes at least
+constexpr int kMinPlaces = 4;                // that a CTA takes at least
 constexpr float kLowest = -3.0e38f;          // of a reference before its first token
 constexpr float kShift = 7.f;                // numerator weights are 2^7 at their reference (mv holds it less 7),
 constexpr float kLazy = 8.f;                 // and a reference moves when one exceeds it by 2^8: below fp16's 2^16
@@ -81,6 +81,13 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+template <typename T>
+__device__ __forceinline__ bool quad_bad(const uint4& v) {
+  return pair_bad<T>(v.x) || pair_bad<T>(v.y) || pair_bad<T>(v.z) || pair_bad<T>(v.w);
+}
 __device__ __forceinline__ float lds32f(uint32_t a) {
   float v;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
@@ -91,18 +98,25 @@ __device__ __forceinline__ float lds32f(uint32_t a) {
 __device__ __forceinline__ bool row_valid(const Q8AttendArgs& a, int len, int nr) {
   return len >= 0 && len <= a.c.capacity && nr >= 0 && nr <= a.n;
 }
-// Places of a unit of row b.
-__device__ __forceinline__ int row_places(const Q8AttendArgs& a, int b) {
-  const int len = a.lens[b], nr = a.n_rows ? a.n_rows[b] : a.n;
-  return row_valid(a, len, nr) && nr > 0 && len > 0 ? kUnitCost + len / kQ8Block + (len % kQ8Block != 0) : 0;
-}
-// Places before each row into pre[0 .. batch] (a unit's places x units of a row).
-__device__ __forceinline__ void plan_rows(const Q8AttendArgs& a, int subs, uint32_t* pre, uint32_t* warp_sums) {
+// In shared memory: places before each row [batch + 1], lengths [batch] (0 where a row has no work).
+struct Plan {
+  uint32_t* pre;
+  int* len;
+};
+// Places before each row (a unit's places x units of a row).
+__device__ __forceinline__ void plan_rows(const Q8AttendArgs& a, int subs, const Plan& p, uint32_t* warp_sums) {
   uint32_t total = 0;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+#pragma unroll 1
   for (int b0 = 0; b0 < a.c.batch; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
-    const uint32_t v = b < a.c.batch ? (uint32_t)row_places(a, b) * subs : 0;
+    uint32_t v = 0;
+    if (b < a.c.batch) {
+      const int len = a.lens[b], nr = a.n_rows ? a.n_rows[b] : a.n;
+      const bool on = row_valid(a, len, nr) && nr > 0 && len > 0;
+      p.len[b] = on ? len : 0;
+      v = on ? (uint32_t)(kUnitCost + (len + kQ8Block - 1) / kQ8Block) * subs : 0;
+    }
     uint32_t s = v;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
@@ -117,66 +131,76 @@ __device__ __forceinline__ void plan_rows(const Q8AttendArgs& a, int subs, uint3
       if (w < warp) before += warp_sums[w];
       total += warp_sums[w];
     }
-    if (b < a.c.batch) pre[b] = before + s - v;
+    if (b < a.c.batch) p.pre[b] = before + s - v;
     __syncthreads();
   }
-  if (threadIdx.x == 0) pre[a.c.batch] = total;
+  if (threadIdx.x == 0) p.pre[a.c.batch] = total;
   __syncthreads();
 }
-__device__ __forceinline__ uint32_t plan_ctas(uint32_t tiles, uint32_t grid) {
-  const uint32_t most = (tiles + kMinTiles - 1) / kMinTiles;
+__device__ __forceinline__ uint32_t plan_ctas(uint32_t places, uint32_t grid) {
+  const uint32_t most = (places + kMinPlaces - 1) / kMinPlaces;
   return most < grid ? most : grid;
 }
-__device__ __forceinline__ uint32_t cta_start(uint32_t c, uint32_t tiles, uint32_t ctas) {
-  return (uint32_t)((uint64_t)c * tiles / ctas);
+__device__ __forceinline__ uint32_t cta_start(uint32_t c, uint32_t places, uint32_t ctas) {
+  return (uint32_t)((uint64_t)c * places / ctas);
 }
 // The CTA whose run holds place t.
-__device__ __forceinline__ uint32_t cta_of(uint32_t t, uint32_t tiles, uint32_t ctas) {
-  return (uint32_t)((((uint64_t)t + 1) * ctas + tiles - 1) / tiles) - 1;
+__device__ __forceinline__ uint32_t cta_of(uint32_t t, uint32_t places, uint32_t ctas) {
+  return (uint32_t)((((uint64_t)t + 1) * ctas + places - 1) / places) - 1;
 }
 
 // A CTA's run, segment by segment: a segment is the run's tiles [begin, end) of one unit (kv head x query
-// group of a row), never empty.
+// group of a row), never empty.  Kept in shared memory, one for what a warp computes and one, ahead of it,
+// for what it fetches, so that the code that moves them is there once: a pass's straight code runs once per
+// unit, and its instruction fetches cost more than its instructions do.
 struct Walk {
   int row, sub;
   uint32_t left;                           // places of the run behind this segment
   int whole, tiles, begin, end;            // of the unit: whole blocks, tiles; of the segment: tiles
-  __device__ void enter(const Q8AttendArgs& a, uint32_t pos) {
-    const int len = a.lens[row];
-    whole = len / kQ8Block;
-    tiles = whole + (len % kQ8Block != 0);
-    const uint32_t take = min(left, (uint32_t)(kUnitCost + tiles) - pos);
-    begin = max((int)pos - kUnitCost, 0);
-    end = (int)(pos + take) - kUnitCost;
-    left -= take;
-  }
-  // To the next segment; false at the end of the run.
-  __device__ bool next(const Q8AttendArgs& a, const uint32_t* pre, int subs) {
-    do {
-      if (left == 0) return false;
-      if (++sub == subs) {
-        sub = 0;
-        do ++row;
-        while (pre[row + 1] == pre[row]);
-      }
-      enter(a, 0);
-    } while (end <= begin);
-    return true;
-  }
-  __device__ bool first(const Q8AttendArgs& a, const uint32_t* pre, int subs, uint32_t t0, uint32_t t1) {
-    int lo = 0, hi = a.c.batch;            // pre[lo] <= t0 < pre[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      (pre[mid] <= t0 ? lo : hi) = mid;
-    }
-    row = lo;
-    const uint32_t off = t0 - pre[row], places = (pre[row + 1] - pre[row]) / subs;
-    sub = off / places;
-    left = t1 - t0;
-    enter(a, off % places);
-    return end > begin || next(a, pre, subs);
-  }
 };
+// To the next segment; begin == end at the end of the run.  The warp's lanes write the same values.
+__device__ __noinline__ void walk_next(Walk* w, Plan p, int subs) {
+  Walk x = *w;
+  do {
+    if (x.left == 0) {
+      x.begin = x.end = 0;
+      break;
+    }
+    if (++x.sub == subs) {
+      x.sub = 0;
+      do ++x.row;
+      while (p.pre[x.row + 1] == p.pre[x.row]);
+      const int len = p.len[x.row];
+      x.whole = len / kQ8Block;
+      x.tiles = x.whole + (len % kQ8Block != 0);
+    }
+    const uint32_t take = min(x.left, (uint32_t)(kUnitCost + x.tiles));
+    x.begin = 0;
+    x.end = (int)take - kUnitCost;
+    x.left -= take;
+  } while (x.end <= x.begin);
+  __syncwarp();
+  *w = x;
+  __syncwarp();
+}
+__device__ __forceinline__ Walk walk_first(const Plan& p, int batch, int subs, uint32_t t0, uint32_t t1) {
+  Walk x;
+  int lo = 0, hi = batch;                  // pre[lo] <= t0 < pre[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    (p.pre[mid] <= t0 ? lo : hi) = mid;
+  }
+  x.row = lo;
+  const uint32_t off = t0 - p.pre[lo], places = (p.pre[lo + 1] - p.pre[lo]) / subs;
+  x.sub = off / places;
+  const uint32_t pos = off % places, take = min(t1 - t0, places - pos);
+  x.tiles = (int)places - kUnitCost;
+  x.whole = p.len[lo] / kQ8Block;
+  x.begin = max((int)pos - kUnitCost, 0);
+  x.end = (int)(pos + take) - kUnitCost;   // <= begin: a run that begins with places alone
+  x.left = t1 - t0 - take;
+  return x;
+}
 
 template <int D, int NT>
 struct Shape {
@@ -185,14 +209,14 @@ struct Shape {
   static constexpr int STAGE = 2 * SLAB + 16;              // K, V, scales
   static constexpr int RING = kWarps * kStages * STAGE;
   static constexpr int OROW = D + 4;                       // a row of partial results: o, ml, mv, l
-  static constexpr int JOIN = 2 * ROWS * OROW * 4;
-  static constexpr int STATS = kWarps * ROWS * 4 * 4;
+  static constexpr int JOIN = kWarps * ROWS * OROW * 4;
+  static constexpr int WALK = kWarps * 2 * (int)sizeof(Walk);
 };
 // CTAs per SM: what registers and shared memory allow.
 constexpr int ctas_per_sm(int d, int nt) { return nt > 1 ? 2 : d == 128 ? 3 : 4; }
 template <int D, int NT>
 int smem_bytes(int batch) {
-  return Shape<D, NT>::RING + Shape<D, NT>::JOIN + Shape<D, NT>::STATS + 16 + 4 * (batch + 1);
+  return Shape<D, NT>::RING + Shape<D, NT>::JOIN + Shape<D, NT>::WALK + 16 + 4 * (2 * batch + 1);
 }
 
 // Byte of 16-byte chunk c of token r in a slab: the chunks are permuted inside
@@ -223,332 +247,288 @@ struct Pass {
   uint32_t qf[NT][KS][2];
   int lane, gid, tig, warp;
 
-  __device__ void start(const Q8AttendArgs& a, int row, int kvh, int r0) {
+  // Query row r of a unit (r = token G + head); rows behind the last one repeat it and are not stored.
+  __device__ __forceinline__ const T* q_row(const Q8AttendArgs& a, int row, int kvh, int r) {
+    r = min(r, a.n * a.G - 1);
+    return static_cast<const T*>(a.q) + row * a.row_stride + r / a.G * a.token_stride +
+           (int64_t)(kvh * a.G + r % a.G) * a.head_stride;
+  }
+
+  // Loads the queries as the B operand, column 8 t + gid, in fp16: a bf16
+  // query is scaled by the power of two that brings its largest element into
+  // [1, 2), which cq takes back.
+  __device__ __forceinline__ void start(const Q8AttendArgs& a, int row, int kvh, int r0, int len) {
 #pragma unroll
     for (int m = 0; m < KS; ++m)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[m][t][e] = 0.f;
-    const int len = a.lens[row], nr = a.n_rows ? a.n_rows[row] : a.n;
-    min_end = len - nr + 1 + r0 / a.G;
+    const int base = len - (a.n_rows ? a.n_rows[row] : a.n) + 1;
+    min_end = base + r0 / a.G;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const T* q = q_row(a, row, kvh, r0 + 8 * t + gid) + 16 * tig;
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint4 v = *reinterpret_cast<const uint4*>(q + 64 * j + 8 * x);
+          qf[t][4 * j + 2 * x][0] = v.x, qf[t][4 * j + 2 * x][1] = v.y;
+          qf[t][4 * j + 2 * x + 1][0] = v.z, qf[t][4 * j + 2 * x + 1][1] = v.w;
+        }
+    }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       float up = a.scale_log2;
-      load_q<true>(a, row, kvh, r0, t, qf[t], up);
+      if (Pair16<T>::kWide) {
+        uint32_t mx = 0;
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+          mx = __vmaxu2(mx, __vmaxu2(qf[t][s][0] & 0x7fff7fffu, qf[t][s][1] & 0x7fff7fffu));
+        mx = max(mx & 0xffffu, mx >> 16);
+        mx = max(mx, __shfl_xor_sync(~0u, mx, 1));
+        mx = max(mx, __shfl_xor_sync(~0u, mx, 2));
+        const int e = mx >= 0x7f80u ? 0 : min(max((int)(mx >> 7) - 127, -126), 126);   // NaN and infinities pass as they are
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+        up *= __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float2 w = unpack16<T>(qf[t][s][x]);
+            qf[t][s][x] = pack16<__half>(w.x * down, w.y * down);
+          }
+      }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         ml[t][j] = mv[t][j] = kLowest;
         l[t][j] = 0.f;
         cq[t][j] = __shfl_sync(~0u, up, 4 * (2 * tig + j));
-        end[t][j] = len - nr + 1 + (r0 + 8 * t + 2 * tig + j) / a.G;
+        end[t][j] = base + (r0 + 8 * t + 2 * tig + j) / a.G;
       }
     }
   }
 
-  // The B operand of query 8 t + gid.  AS_HALF: fp16 whatever the type; a bf16
-  // query is scaled by the power of two that brings its largest element into
-  // [1, 2), and `up` takes that factor back.
-  template <bool AS_HALF>
-  __device__ void load_q(const Q8AttendArgs& a, int row, int kvh, int r0, int t, uint32_t (&f)[KS][2], float& up) {
-    const int r = r0 + 8 * t + gid;
-    const bool on = r < a.n * a.G;
-    const int i = on ? r / a.G : 0, h = on ? r % a.G : 0;
-    const T* q = static_cast<const T*>(a.q) + row * a.row_stride + i * a.token_stride +
-                 (int64_t)(kvh * a.G + h) * a.head_stride;
-#pragma unroll
-    for (int j = 0; j < D / 64; ++j)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const uint4 v = on ? *reinterpret_cast<const uint4*>(q + 64 * j + 16 * tig + 8 * x) : make_uint4(0, 0, 0, 0);
-        f[4 * j + 2 * x][0] = v.x, f[4 * j + 2 * x][1] = v.y;
-        f[4 * j + 2 * x + 1][0] = v.z, f[4 * j + 2 * x + 1][1] = v.w;
-      }
-    if (AS_HALF && Pair16<T>::kWide) {
-      uint32_t mx = 0;
-#pragma unroll
-      for (int s = 0; s < KS; ++s) mx = __vmaxu2(mx, __vmaxu2(f[s][0] & 0x7fff7fffu, f[s][1] & 0x7fff7fffu));
-      mx = max(mx & 0xffffu, mx >> 16);
-      mx = max(mx, __shfl_xor_sync(~0u, mx, 1));
-      mx = max(mx, __shfl_xor_sync(~0u, mx, 2));
-      int e = (int)(mx >> 7) - 127;                        // of the largest element
-      e = mx >= 0x7f80u ? 0 : max(e, -126);                // NaN and infinities pass as they are
-      const float down = __uint_as_float((uint32_t)(127 - min(e, 126)) << 23);
-      up *= __uint_as_float((uint32_t)(127 + min(e, 126)) << 23);
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float2 w = unpack16<T>(f[s][x]);
-          f[s][x] = pack16<__half>(w.x * down, w.y * down);
-        }
-    }
-  }
-
-  // Weights of 16 tokens from their logits, c_p = x_p / f.  VIS: positions
-  // first + gid (+ 8) may be behind a query's end, or bad (bits of `bad`).
-  // Returns the numerator's weights in `w` (denominators are added here).
-  template <bool VIS>
+  // Weights of 16 tokens from their logits: denominators are added up here,
+  // the numerators' are returned in `w`.  MASK: a token at position first +
+  // gid (+ 8) counts only before a query's end.
   __device__ __forceinline__ void weights(const float (&s)[NT][4], const float (&f)[NT][2], float lsv, int first,
-                                          uint32_t bad, float (&w)[NT][4]) {
+                                          bool mask, float (&w)[NT][4]) {
     float pl[NT][4];
     float top_l = kLowest, top_v = kLowest;
+    auto spread = [&]() {
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = e & 1;
-        pl[t][e] = fmaf(s[t][e], f[t][j], -ml[t][j]);
-        w[t][e] = fmaf(s[t][e], f[t][j], lsv - mv[t][j]);
-        const bool vis = !VIS || first + gid + 8 * (e >> 1) < end[t][j];
-        if (vis) top_l = fmaxf(top_l, pl[t][e]), top_v = fmaxf(top_v, w[t][e]);
-      }
-    if (__any_sync(~0u, top_l > kLazy || top_v > kLazy + kShift)) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float x0 = s[t][j] * f[t][j], x1 = s[t][j + 2] * f[t][j];
-          if (VIS) {
-            if (first + gid >= end[t][j]) x0 = kLowest;
-            if (first + gid + 8 >= end[t][j]) x1 = kLowest;
-          }
-          float mx = fmaxf(x0, x1);
-#pragma unroll
-          for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
-          const float nl = fmaxf(ml[t][j], mx), nv = mx > kLowest ? fmaxf(mv[t][j], mx + lsv - kShift) : mv[t][j];
-          l[t][j] *= ex2(ml[t][j] - nl);
-          const float c = ex2(mv[t][j] - nv);
-          ml[t][j] = nl;
-          mv[t][j] = nv;
-#pragma unroll
-          for (int m = 0; m < KS; ++m) o[m][t][j] *= c, o[m][t][j + 2] *= c;
-        }
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           pl[t][e] = fmaf(s[t][e], f[t][e & 1], -ml[t][e & 1]);
           w[t][e] = fmaf(s[t][e], f[t][e & 1], lsv - mv[t][e & 1]);
         }
-      }
+      if (mask)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (first + gid + 8 * (e >> 1) >= end[t][e & 1]) pl[t][e] = w[t][e] = -INFINITY;
+    };
+    spread();
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top_l = fmaxf(top_l, pl[t][e]), top_v = fmaxf(top_v, w[t][e]);
+    if (__any_sync(~0u, top_l > kLazy || top_v > kLazy + kShift)) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          // -inf: masked
+          float mx = fmaxf(pl[t][j] == -INFINITY ? kLowest : s[t][j] * f[t][j],
+                           pl[t][j + 2] == -INFINITY ? kLowest : s[t][j + 2] * f[t][j]);
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
+          const float nl = fmaxf(ml[t][j], mx), nv = mx > kLowest ? fmaxf(mv[t][j], mx + lsv - kShift) : mv[t][j];
+          l[t][j] *= ex2(ml[t][j] - nl);
+          const float c = ex2(mv[t][j] - nv);
+          ml[t][j] = nl, mv[t][j] = nv;
+#pragma unroll
+          for (int m = 0; m < KS; ++m) o[m][t][j] *= c, o[m][t][j + 2] *= c;
+        }
+      spread();
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float p = ex2(pl[t][e]);
+        l[t][e & 1] += ex2(pl[t][e]);
         w[t][e] = ex2(w[t][e]);
-        if (VIS) {
-          const bool vis = first + gid + 8 * (e >> 1) < end[t][e & 1];
-          const bool nan = bad >> (gid + 8 * (e >> 1)) & 1;
-          p = !vis ? 0.f : nan ? NAN : p;
-          w[t][e] = !vis ? 0.f : nan ? NAN : w[t][e];
-        }
-        l[t][e & 1] += p;
       }
   }
 
-  // 16 tokens of a whole block from the ring stage at `st`, scales behind it.
-  template <bool VIS>
-  __device__ __forceinline__ void codes(uint32_t st, int first) {
+  // The warp's 16 tokens of a tile: of a whole block, from the ring stage at
+  // `st` with the scales behind it, or of the open block, from the 16-bit
+  // ring in global memory.  The open block's products take the cache's own
+  // type, exactly; bf16 weights go in as two bf16 parts.
+  __device__ __forceinline__ void tile(const Q8AttendArgs& a, uint32_t st, int tile, bool open, int row, int kvh,
+                                       int r0, int len) {
     constexpr int SLAB = Shape<D, NT>::SLAB;
-    float s[NT][4];
+    const int first = tile * kQ8Block + 16 * warp, cnt = len - first;
+    if (cnt <= 0) return;                                  // behind the open block's tokens
+    const size_t ring = (((size_t)row * a.c.num_kv_heads + kvh) * kQ8Ring + first % kQ8Ring) * D;
+    float s[NT][4], f[NT][2], w[NT][4], lsv = 0.f;
+    uint32_t bad = 0;                                      // the open block's tokens with a NaN or an infinity
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
-    const float sk = lds32f(st + 2 * SLAB), sv = lds32f(st + 2 * SLAB + 4);
+    if (!open) {
+      const float sk = lds32f(st + 2 * SLAB);
+      lsv = lg2(lds32f(st + 2 * SLAB + 4));
 #pragma unroll
-    for (int j = 0; j < D / 64; ++j) {
-      const uint4 ka = lds128(st + slab_at<D>(gid, tig + 4 * j)), kb = lds128(st + slab_at<D>(gid + 8, tig + 4 * j));
-      const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+      for (int t = 0; t < NT; ++t) f[t][0] = sk * cq[t][0], f[t][1] = sk * cq[t][1];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        uint32_t a0, a1, a2, a3;
-        codes_to_half4<FMT>(wa[x], a0, a2);
-        codes_to_half4<FMT>(wb[x], a1, a3);
+      for (int j = 0; j < D / 64; ++j) {
+        const uint4 ka = lds128(st + slab_at<D>(gid, tig + 4 * j)), kb = lds128(st + slab_at<D>(gid + 8, tig + 4 * j));
+        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
-        for (int t = 0; t < NT; ++t) mma16816(s[t], a0, a1, a2, a3, qf[t][4 * j + x][0], qf[t][4 * j + x][1], __half());
+        for (int x = 0; x < 4; ++x) {
+          uint32_t a0, a1, a2, a3;
+          codes_to_half4<FMT>(wa[x], a0, a2);
+          codes_to_half4<FMT>(wb[x], a1, a3);
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            mma16816(s[t], a0, a1, a2, a3, qf[t][4 * j + x][0], qf[t][4 * j + x][1], __half());
+        }
       }
-    }
-    float f[NT][2], w[NT][4];
+    } else {
+      const T* kr = static_cast<const T*>(a.c.k_recent) + ring + 16 * tig;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) f[t][0] = sk * cq[t][0], f[t][1] = sk * cq[t][1];
-    weights<VIS>(s, f, lg2(sv), first, 0u, w);
-    uint32_t b[NT][2];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      b[t][0] = movmatrix(pack16<__half>(w[t][0], w[t][1]));
-      b[t][1] = movmatrix(pack16<__half>(w[t][2], w[t][3]));
-    }
-    uint32_t v[4][D / 32];                                 // tokens 2 tig, 2 tig + 1, + 8, + 9
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 2 * tig + (i & 1) + 8 * (i >> 1);
-      if (D == 128) {
-        const uint4 x = lds128(st + SLAB + slab_at<D>(r, gid));
-        v[i][0] = x.x, v[i][1] = x.y, v[i][D / 32 - 2] = x.z, v[i][D / 32 - 1] = x.w;
-      } else {
-        const uint2 x = lds64(st + SLAB + slab_at<D>(r, gid >> 1) + 8 * (gid & 1));
-        v[i][0] = x.x, v[i][1] = x.y;
-      }
-    }
-#pragma unroll
-    for (int x = 0; x < D / 32; ++x)
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const uint32_t lo = __byte_perm(v[0][x], v[1][x], y ? 0x7362 : 0x5140);
-        const uint32_t hi = __byte_perm(v[2][x], v[3][x], y ? 0x7362 : 0x5140);
-        uint32_t a0, a1, a2, a3;
-        codes_to_half4<FMT>(lo, a0, a1);
-        codes_to_half4<FMT>(hi, a2, a3);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) mma16816(o[2 * x + y][t], a0, a1, a2, a3, b[t][0], b[t][1], __half());
-      }
-  }
-
-  // The warp's 16 tokens of the open block, from the 16-bit ring.  Its products
-  // take the cache's own type, exactly; bf16 weights go in as two bf16 parts.
-  __device__ void open(const Q8AttendArgs& a, int row, int kvh, int r0, int whole) {
-    const int cnt = a.lens[row] - whole * kQ8Block - 16 * warp;  // tokens of this warp
-    if (cnt <= 0) return;
-    const size_t unit = (size_t)row * a.c.num_kv_heads + kvh;
-    const size_t base = (unit * kQ8Ring + (whole & 1) * kQ8Block + 16 * warp) * D;
-    const T *kr = static_cast<const T*>(a.c.k_recent) + base, *vr = static_cast<const T*>(a.c.v_recent) + base;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    uint32_t bad = 0;
-    float s[NT][4];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
-    uint32_t k[2][KS][2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int t = 0; t < NT; ++t) f[t][0] = f[t][1] = a.scale_log2;
 #pragma unroll
       for (int j = 0; j < D / 64; ++j)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const uint4 w = gid + 8 * i < cnt ? *reinterpret_cast<const uint4*>(kr + (gid + 8 * i) * D + 64 * j + 16 * tig + 8 * x) : zero;
-          k[i][4 * j + 2 * x][0] = w.x, k[i][4 * j + 2 * x][1] = w.y;
-          k[i][4 * j + 2 * x + 1][0] = w.z, k[i][4 * j + 2 * x + 1][1] = w.w;
-          if (pair_bad<T>(w.x) || pair_bad<T>(w.y) || pair_bad<T>(w.z) || pair_bad<T>(w.w)) bad |= 1u << (gid + 8 * i);
+          uint4 k[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = gid + 8 * i;
+            k[i] = r < cnt ? *reinterpret_cast<const uint4*>(kr + r * D + 64 * j + 8 * x) : make_uint4(0, 0, 0, 0);
+            if (quad_bad<T>(k[i])) bad |= 1u << r;
+          }
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            uint32_t b[2][2];
+            if (Pair16<T>::kWide) {                        // the raw query: cached by the load of qf
+              const uint4 v = *reinterpret_cast<const uint4*>(q_row(a, row, kvh, r0 + 8 * t + gid) + 64 * j + 16 * tig + 8 * x);
+              b[0][0] = v.x, b[0][1] = v.y, b[1][0] = v.z, b[1][1] = v.w;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) b[e][0] = qf[t][4 * j + 2 * x + e][0], b[e][1] = qf[t][4 * j + 2 * x + e][1];
+            }
+            mma16816(s[t], k[0].x, k[1].x, k[0].y, k[1].y, b[0][0], b[0][1], T());
+            mma16816(s[t], k[0].z, k[1].z, k[0].w, k[1].w, b[1][0], b[1][1], T());
+          }
         }
-    uint32_t v[4][KS];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 2 * tig + (i & 1) + 8 * (i >> 1);
-#pragma unroll
-      for (int x = 0; x < KS / 4; ++x) {
-        const uint4 w = r < cnt ? *reinterpret_cast<const uint4*>(vr + r * D + D / 8 * gid + 8 * x) : zero;
-        v[i][4 * x] = w.x, v[i][4 * x + 1] = w.y, v[i][4 * x + 2] = w.z, v[i][4 * x + 3] = w.w;
-        if (pair_bad<T>(w.x) || pair_bad<T>(w.y) || pair_bad<T>(w.z) || pair_bad<T>(w.w)) bad |= 1u << r;
-      }
     }
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      uint32_t raw[KS][2];
-      float unused = 0.f;
-      if (Pair16<T>::kWide) load_q<false>(a, row, kvh, r0, t, raw, unused);
-#pragma unroll
-      for (int x = 0; x < KS; ++x)
-        mma16816(s[t], k[0][x][0], k[1][x][0], k[0][x][1], k[1][x][1], Pair16<T>::kWide ? raw[x][0] : qf[t][x][0],
-                 Pair16<T>::kWide ? raw[x][1] : qf[t][x][1], T());
-    }
-    bad = __reduce_or_sync(~0u, bad);
-    if (bad) {                                             // 0 x NaN would reach queries that do not see the token
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (bad >> (2 * tig + (i & 1) + 8 * (i >> 1)) & 1)
-#pragma unroll
-          for (int x = 0; x < KS; ++x) v[i][x] = 0;
-    }
-    float f[NT][2], w[NT][4];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) f[t][0] = f[t][1] = a.scale_log2;
-    weights<true>(s, f, 0.f, whole * kQ8Block + 16 * warp, bad, w);
-#pragma unroll
-    for (int part = 0; part < (Pair16<T>::kWide ? 2 : 1); ++part) {
+    weights(s, f, lsv, first, open || (tile + 1) * kQ8Block > min_end, w);
+    if (!open) {
       uint32_t b[NT][2];
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < NT; ++t) {
+        b[t][0] = movmatrix(pack16<__half>(w[t][0], w[t][1]));
+        b[t][1] = movmatrix(pack16<__half>(w[t][2], w[t][3]));
+      }
+      uint32_t v[4][D / 32];                               // tokens 2 tig, 2 tig + 1, + 8, + 9
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t pk = pack16<T>(w[t][2 * e], w[t][2 * e + 1]);
-          b[t][e] = movmatrix(pk);
-          const float2 r = unpack16<T>(pk);
-          w[t][2 * e] -= r.x, w[t][2 * e + 1] -= r.y;
+      for (int i = 0; i < 4; ++i) {
+        const int r = 2 * tig + (i & 1) + 8 * (i >> 1);
+        if (D == 128) {
+          const uint4 x = lds128(st + SLAB + slab_at<D>(r, gid));
+          v[i][0] = x.x, v[i][1] = x.y, v[i][D / 32 - 2] = x.z, v[i][D / 32 - 1] = x.w;
+        } else {
+          const uint2 x = lds64(st + SLAB + slab_at<D>(r, gid >> 1) + 8 * (gid & 1));
+          v[i][0] = x.x, v[i][1] = x.y;
         }
+      }
 #pragma unroll
-      for (int x = 0; x < KS; ++x) {
-        const uint32_t a0 = __byte_perm(v[0][x], v[1][x], 0x5410), a1 = __byte_perm(v[0][x], v[1][x], 0x7632);
-        const uint32_t a2 = __byte_perm(v[2][x], v[3][x], 0x5410), a3 = __byte_perm(v[2][x], v[3][x], 0x7632);
+      for (int x = 0; x < D / 32; ++x)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) mma16816(o[x][t], a0, a1, a2, a3, b[t][0], b[t][1], T());
+        for (int y = 0; y < 2; ++y) {
+          const uint32_t lo = __byte_perm(v[0][x], v[1][x], y ? 0x7362 : 0x5140);
+          const uint32_t hi = __byte_perm(v[2][x], v[3][x], y ? 0x7362 : 0x5140);
+          uint32_t a0, a1, a2, a3;
+          codes_to_half4<FMT>(lo, a0, a1);
+          codes_to_half4<FMT>(hi, a2, a3);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma16816(o[2 * x + y][t], a0, a1, a2, a3, b[t][0], b[t][1], __half());
+        }
+    } else {
+      const T* vr = static_cast<const T*>(a.c.v_recent) + ring + D / 8 * gid;
+      uint4 v[4][KS / 4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 2 * tig + (i & 1) + 8 * (i >> 1);
+#pragma unroll
+        for (int x = 0; x < KS / 4; ++x) {
+          v[i][x] = r < cnt ? *reinterpret_cast<const uint4*>(vr + r * D + 8 * x) : make_uint4(0, 0, 0, 0);
+          if (quad_bad<T>(v[i][x])) bad |= 1u << r;
+        }
+      }
+      bad = __reduce_or_sync(~0u, bad);
+      if (bad) {
+        // NaN for the queries that see the token; 0 x NaN would reach the others, so its values go
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (bad >> (2 * tig + (i & 1) + 8 * (i >> 1)) & 1)
+#pragma unroll
+            for (int x = 0; x < KS / 4; ++x) v[i][x] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if ((bad >> (gid + 8 * (e >> 1)) & 1) && first + gid + 8 * (e >> 1) < end[t][e & 1]) w[t][e] = NAN;
+      }
+#pragma unroll
+      for (int part = 0; part < (Pair16<T>::kWide ? 2 : 1); ++part) {
+        uint32_t b[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t pk = pack16<T>(w[t][2 * e], w[t][2 * e + 1]);
+            b[t][e] = movmatrix(pk);
+            const float2 r = unpack16<T>(pk);
+            w[t][2 * e] -= r.x, w[t][2 * e + 1] -= r.y;
+          }
+#pragma unroll
+        for (int x = 0; x < KS; ++x) {
+          const uint32_t v0 = word(v[0][x / 4], x % 4), v1 = word(v[1][x / 4], x % 4);
+          const uint32_t v2 = word(v[2][x / 4], x % 4), v3 = word(v[3][x / 4], x % 4);
+          const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632);
+          const uint32_t a2 = __byte_perm(v2, v3, 0x5410), a3 = __byte_perm(v2, v3, 0x7632);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma16816(o[x][t], a0, a1, a2, a3, b[t][0], b[t][1], T());
+        }
       }
     }
   }
 
-  // Joins the four warps' results into warp 0's registers (o, ml, mv, l).
-  __device__ void join(float* area, float* stats) {
+  // The warp's results into its rows of the join area.
+  __device__ __forceinline__ void leave(float* area) {
     constexpr int ROWS = Shape<D, NT>::ROWS, OROW = Shape<D, NT>::OROW;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
+        float* p = area + (warp * ROWS + 8 * t + 2 * tig + j) * OROW;
 #pragma unroll
         for (int d = 4; d < 32; d *= 2) l[t][j] += __shfl_xor_sync(~0u, l[t][j], d);
-        if (gid == 0) {
-          float* p = stats + (warp * ROWS + 8 * t + 2 * tig + j) * 4;
-          p[0] = ml[t][j], p[1] = mv[t][j], p[2] = l[t][j];
-        }
+        if (gid == 0) p[D] = ml[t][j], p[D + 1] = mv[t][j], p[D + 2] = l[t][j];
+#pragma unroll
+        for (int m = 0; m < KS; m += 2)
+          *reinterpret_cast<float4*>(p + D / 8 * gid + 2 * m) =
+              make_float4(o[m][t][j], o[m][t][j + 2], o[m + 1][t][j], o[m + 1][t][j + 2]);
       }
-    __syncthreads();
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float gl = kLowest, gv = kLowest, sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float* p = stats + (w * ROWS + 8 * t + 2 * tig + j) * 4;
-          gl = fmaxf(gl, p[0]), gv = fmaxf(gv, p[1]);
-        }
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float* p = stats + (w * ROWS + 8 * t + 2 * tig + j) * 4;
-          sum += p[2] * ex2(p[0] - gl);
-        }
-        const float c = ex2(mv[t][j] - gv);
-#pragma unroll
-        for (int m = 0; m < KS; ++m) o[m][t][j] *= c, o[m][t][j + 2] *= c;
-        ml[t][j] = gl, mv[t][j] = gv, l[t][j] = sum;
-      }
-#pragma unroll
-    for (int half = 2; half >= 1; half /= 2) {
-      if (warp >= half && warp < 2 * half) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int m = 0; m < KS; ++m)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              *reinterpret_cast<float2*>(area + ((warp - half) * ROWS + 8 * t + 2 * tig + j) * OROW + D / 8 * gid + 2 * m) =
-                  make_float2(o[m][t][j], o[m][t][j + 2]);
-      }
-      __syncthreads();
-      if (warp < half) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int m = 0; m < KS; ++m)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float2 x = *reinterpret_cast<const float2*>(area + (warp * ROWS + 8 * t + 2 * tig + j) * OROW + D / 8 * gid + 2 * m);
-              o[m][t][j] += x.x, o[m][t][j + 2] += x.y;
-            }
-      }
-      __syncthreads();
-    }
   }
 };
 
@@ -561,49 +541,53 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q8_attend_kernel
   using S = Shape<D, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   float* area = reinterpret_cast<float*>(smem + S::RING);
-  float* stats = reinterpret_cast<float*>(smem + S::RING + S::JOIN);
-  uint32_t* sums = reinterpret_cast<uint32_t*>(smem + S::RING + S::JOIN + S::STATS);
-  uint32_t* pre = sums + 4;
+  Walk* walks = reinterpret_cast<Walk*>(smem + S::RING + S::JOIN);
+  uint32_t* sums = reinterpret_cast<uint32_t*>(smem + S::RING + S::JOIN + S::WALK);
+  const Plan plan{sums + 4, reinterpret_cast<int*>(sums + 4 + a.c.batch + 1)};
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int groups = (a.n * a.G + S::ROWS - 1) / S::ROWS, subs = a.c.num_kv_heads * groups;
-  plan_rows(a, subs, pre, sums);
+  plan_rows(a, subs, plan, sums);
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < a.c.batch; b += kThreads)
       if (!row_valid(a, a.lens[b], a.n_rows ? a.n_rows[b] : a.n)) atomicOr(a.c.status, kQ8StatusInvalid);
-  const uint32_t tiles = pre[a.c.batch], ctas = plan_ctas(tiles, gridDim.x);
+  const uint32_t places = plan.pre[a.c.batch], ctas = plan_ctas(places, gridDim.x);
   if (blockIdx.x >= ctas) return;
-  const uint32_t t0 = cta_start(blockIdx.x, tiles, ctas), t1 = cta_start(blockIdx.x + 1, tiles, ctas);
+  const uint32_t t0 = cta_start(blockIdx.x, places, ctas), t1 = cta_start(blockIdx.x + 1, places, ctas);
 
   Pass<T, FMT, D, NT> ps;
   ps.lane = threadIdx.x % 32, ps.warp = threadIdx.x / 32;
   ps.gid = ps.lane / 4, ps.tig = ps.lane % 4;
   const uint32_t ring = smem_u32(smem) + ps.warp * kStages * S::STAGE;
+  Walk *get = walks + 2 * ps.warp, *use = get + 1;
+  *get = walk_first(plan, a.c.batch, subs, t0, t1);
+  __syncwarp();
+  if (get->end <= get->begin) walk_next(get, plan, subs);
+  *use = *get;
+  __syncwarp();
+
   // The warp's 16 tokens of the run's next whole block go to a stage of the warp's ring (open blocks are
   // read where they are used): 16-byte copies from kp, vp, and the two scales.
-  Walk get;
   const uint8_t *kp = nullptr, *vp = nullptr;
   const float* sp = nullptr;
   int more = 0;                                            // whole blocks to fetch from kp, vp on
-  auto aim = [&](bool on) {
-    for (; on; on = get.next(a, pre, subs)) {
-      more = min(get.end, get.whole) - get.begin;
-      if (more <= 0) continue;
-      const size_t unit = (size_t)get.row * a.c.num_kv_heads + get.sub / groups;
-      const size_t at = (unit * a.c.capacity + (size_t)get.begin * kQ8Block + 16 * ps.warp) * D + 16 * ps.lane;
-      kp = static_cast<const uint8_t*>(a.c.k_codes) + at;
-      vp = static_cast<const uint8_t*>(a.c.v_codes) + at;
-      sp = (ps.lane ? a.c.v_scales : a.c.k_scales) + unit * (a.c.capacity / kQ8Block) + get.begin;
-      return;
-    }
-    more = 0;
-  };
   uint32_t dst[S::SLAB / 512];
 #pragma unroll
   for (int i = 0; i < S::SLAB / 512; ++i) {
     const int x = i * 32 + ps.lane;
     dst[i] = slab_at<D>(x / (D / 16), x % (D / 16));
   }
+  bool fresh = true;                                       // `get` is at a segment that kp, vp have not begun
   auto fetch = [&](uint32_t st) {
+    while (more == 0 && get->begin < get->end) {
+      if (!fresh) walk_next(get, plan, subs);
+      fresh = false;
+      more = max(min(get->end, get->whole) - get->begin, 0);
+      const size_t unit = (size_t)get->row * a.c.num_kv_heads + get->sub / groups;
+      const size_t at = (unit * a.c.capacity + (size_t)get->begin * kQ8Block + 16 * ps.warp) * D + 16 * ps.lane;
+      kp = static_cast<const uint8_t*>(a.c.k_codes) + at;
+      vp = static_cast<const uint8_t*>(a.c.v_codes) + at;
+      sp = (ps.lane ? a.c.v_scales : a.c.k_scales) + unit * (a.c.capacity / kQ8Block) + get->begin;
+    }
     if (more > 0) {
 #pragma unroll
       for (int i = 0; i < S::SLAB / 512; ++i) {
@@ -612,63 +596,77 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q8_attend_kernel
       }
       if (ps.lane < 2) cp_async4(st + 2 * S::SLAB + 4 * ps.lane, sp);
       kp += kQ8Block * D, vp += kQ8Block * D, ++sp;
-      if (--more == 0) aim(get.next(a, pre, subs));
+      --more;
     }
     cp_commit();
   };
-  Walk use;
-  bool on = use.first(a, pre, subs, t0, t1);
-  get = use;
-  aim(on);
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) fetch(ring + i * S::STAGE);
 
-  uint32_t st = ring, ahead = ring + (kStages - 1) * S::STAGE;
-  for (; on; on = use.next(a, pre, subs)) {
-    const int kvh = use.sub / groups, r0 = use.sub % groups * S::ROWS;
-    ps.start(a, use.row, kvh, r0);
-    const int blocks = min(use.end, use.whole);
-    for (int tile = use.begin; tile < blocks; ++tile) {
-      fetch(ahead);
+  // `lag` fetches run ahead before the first tile is used.
+  uint32_t st = ring, ahead = ring;
+  int lag = kStages - 1;
+#pragma unroll 1
+  while (use->begin < use->end) {
+    const int row = use->row, kvh = use->sub / groups, r0 = use->sub % groups * S::ROWS, len = plan.len[row];
+    const int begin = use->begin, end = use->end, whole = use->whole;
+    bool started = false;
+#pragma unroll 1
+    for (int tile = begin; tile < end;) {
+      const bool open = tile >= whole;
+      if (!open || lag > 0) {
+        fetch(ahead);
+        ahead = ahead == ring + (kStages - 1) * S::STAGE ? ring : ahead + S::STAGE;
+        if (lag > 0) {
+          --lag;
+          continue;
+        }
+      }
+      if (!started) ps.start(a, row, kvh, r0, len), started = true;
       cp_wait<kStages - 1>();
       __syncwarp();
-      const int first = tile * kQ8Block + 16 * ps.warp;
-      if ((tile + 1) * kQ8Block <= ps.min_end) ps.template codes<false>(st, first);
-      else ps.template codes<true>(st, first);
+      ps.tile(a, st, tile, open, row, kvh, r0, len);
       __syncwarp();                                        // every lane has read before the stage is filled again
-      ahead = st;
-      st = st == ring + (kStages - 1) * S::STAGE ? ring : st + S::STAGE;
+      if (!open) st = st == ring + (kStages - 1) * S::STAGE ? ring : st + S::STAGE;
+      ++tile;
     }
-    if (use.end > use.whole) ps.open(a, use.row, kvh, r0, use.whole);
-    ps.join(area, stats);
-    if (ps.warp == 0) {
-      const bool all = use.begin == 0 && use.end == use.tiles;
-      // its second result where the unit begins inside the run: of two units that the run shares, one does
-      const uint32_t unit0 = pre[use.row] + (uint32_t)use.sub * (kUnitCost + use.tiles) + kUnitCost;
-      float* part = reinterpret_cast<float*>(a.scratch) + ((size_t)blockIdx.x * 2 + (t0 < unit0)) * S::ROWS * S::OROW;
-      const int nr = a.n_rows ? a.n_rows[use.row] : a.n;
+    ps.leave(area);
+    __syncthreads();
+    // all threads: the four warps' rows together, D / 128 dims of a row each
+    const bool all = begin == 0 && end == use->tiles;
+    // the run's second result where the unit begins inside it: of two units that a run has parts of, one does
+    const uint32_t unit0 = plan.pre[row] + (uint32_t)use->sub * (kUnitCost + use->tiles) + kUnitCost;
+    float* part = reinterpret_cast<float*>(a.scratch) + ((size_t)blockIdx.x * 2 + (t0 < unit0)) * S::ROWS * S::OROW;
+    const int rows = min(S::ROWS, (a.n_rows ? a.n_rows[row] : a.n) * a.G - r0);
+#pragma unroll 1
+    for (int x = threadIdx.x; x < rows * (D / 4); x += kThreads) {
+      const int r = x / (D / 4), d = x % (D / 4) * 4;
+      const float* p = area + r * S::OROW;
+      float gl = kLowest, gv = kLowest, sum = 0.f;
+      float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int q = 0; q < NT; ++q)
+      for (int w = 0; w < kWarps; ++w) {
+        gl = fmaxf(gl, p[w * S::ROWS * S::OROW + D]);
+        gv = fmaxf(gv, p[w * S::ROWS * S::OROW + D + 1]);
+      }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int r = 8 * q + 2 * ps.tig + j, i = (r0 + r) / a.G, h = (r0 + r) % a.G;
-          if (i >= nr) continue;
-          if (all) {
-            T* out = static_cast<T*>(a.out) + (((size_t)use.row * a.n + i) * a.Hq + kvh * a.G + h) * D + D / 8 * ps.gid;
-#pragma unroll
-            for (int m = 0; m < D / 16; ++m)
-              reinterpret_cast<uint32_t*>(out)[m] =
-                  pack16<T>(result(ps.o[m][q][j], ps.ml[q][j], ps.mv[q][j], ps.l[q][j]),
-                            result(ps.o[m][q][j + 2], ps.ml[q][j], ps.mv[q][j], ps.l[q][j]));
-          } else {
-            float* p = part + r * S::OROW;
-#pragma unroll
-            for (int m = 0; m < D / 16; ++m)
-              *reinterpret_cast<float2*>(p + D / 8 * ps.gid + 2 * m) = make_float2(ps.o[m][q][j], ps.o[m][q][j + 2]);
-            if (ps.gid == 0) *reinterpret_cast<float4*>(p + D) = make_float4(ps.ml[q][j], ps.mv[q][j], ps.l[q][j], 0.f);
-          }
-        }
+      for (int w = 0; w < kWarps; ++w) {
+        const float* pw = p + w * S::ROWS * S::OROW;
+        sum += pw[D + 2] * ex2(pw[D] - gl);
+        const float c = ex2(pw[D + 1] - gv);
+        const float4 v = *reinterpret_cast<const float4*>(pw + d);
+        t.x += v.x * c, t.y += v.y * c, t.z += v.z * c, t.w += v.w * c;
+      }
+      if (all) {
+        const int i = (r0 + r) / a.G, h = kvh * a.G + (r0 + r) % a.G;
+        T* out = static_cast<T*>(a.out) + (((size_t)row * a.n + i) * a.Hq + h) * D + d;
+        const float c = sum == 0.f ? 0.f : ex2(gv - gl) / sum;
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack16<T>(t.x * c, t.y * c), pack16<T>(t.z * c, t.w * c));
+      } else {
+        *reinterpret_cast<float4*>(part + r * S::OROW + d) = t;
+        if (d == 0) *reinterpret_cast<float4*>(part + r * S::OROW + D) = make_float4(gl, gv, sum, 0.f);
+      }
     }
+    walk_next(use, plan, subs);
+    __syncthreads();
   }
 }
 
@@ -683,11 +681,12 @@ __global__ void __launch_bounds__(kThreads) q8_join_kernel(const Q8AttendArgs a,
   using S = Shape<D, NT>;
   constexpr int E = D / 32;
   extern __shared__ uint32_t pre[];
+  const Plan plan{pre, reinterpret_cast<int*>(pre + a.c.batch + 1)};
   __shared__ uint32_t sums[kWarps];
   __shared__ float wm[kWarps][3], wo[kWarps][D];
   const int R = a.n * a.G, groups = (R + S::ROWS - 1) / S::ROWS, subs = a.c.num_kv_heads * groups;
   const int row = blockIdx.y, kvh = blockIdx.x / R, r = blockIdx.x % R, i = r / a.G;
-  plan_rows(a, subs, pre, sums);
+  plan_rows(a, subs, plan, sums);
   const int len = a.lens[row], nr = a.n_rows ? a.n_rows[row] : a.n;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const bool valid = row_valid(a, len, nr);
@@ -774,7 +773,7 @@ uint32_t grid_of(const tq_q8_cache& c, int Hq, int n, int num_sms) {
   const int rows = n * (Hq / c.num_kv_heads), nt = pick_nt(rows);
   const int64_t tiles = (int64_t)c.batch * c.num_kv_heads * ((rows + 8 * nt - 1) / (8 * nt)) *
                         (c.capacity / kQ8Block + kUnitCost);
-  const int64_t most = (int64_t)num_sms * ctas_per_sm(c.head_dim, nt), want = (tiles + kMinTiles - 1) / kMinTiles;
+  const int64_t most = (int64_t)num_sms * ctas_per_sm(c.head_dim, nt), want = (tiles + kMinPlaces - 1) / kMinPlaces;
   return (uint32_t)(want < most ? want : most);
 }
 
@@ -791,7 +790,7 @@ cudaError_t launch(const Q8AttendArgs& a, uint32_t grid, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.c.num_kv_heads * a.n * a.G), (unsigned)a.c.batch);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = 4 * (a.c.batch + 1);
+  cfg.dynamicSmemBytes = 4 * (2 * a.c.batch + 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
