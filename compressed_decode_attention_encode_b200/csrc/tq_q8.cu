@@ -118,7 +118,9 @@ __global__ void __launch_bounds__(kAppendThreads) q8_append_kernel(const Q8Appen
 }
 
 // ---- read -----------------------------------------------------------------
-constexpr int kReadThreads = 256;
+// A thread takes kReadItems chunks of 8 values, the loads of all of them
+// before any conversion.
+constexpr int kReadThreads = 256, kReadItems = 4;
 
 template <typename T, int FMT, int D>
 __global__ void __launch_bounds__(kReadThreads) q8_read_kernel(const Q8ReadArgs a) {
@@ -129,65 +131,98 @@ __global__ void __launch_bounds__(kReadThreads) q8_read_kernel(const Q8ReadArgs 
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.c.status, kQ8StatusInvalid);
     return;
   }
-  const int64_t i = (int64_t)blockIdx.x * kReadThreads + threadIdx.x;
-  const int64_t t = i / CH, p = a.start + t;
-  const int c = (int)(i % CH);
-  if (t >= a.n || p >= len) return;
-  uint4 r;
-  if (p >= len / kQ8Block * kQ8Block) {
-    r = reinterpret_cast<const uint4*>(kv ? a.c.v_recent : a.c.k_recent)[((size_t)unit * kQ8Ring + p % kQ8Ring) * CH + c];
-  } else {
-    const float s = (kv ? a.c.v_scales : a.c.k_scales)[(size_t)unit * (a.c.capacity / kQ8Block) + p / kQ8Block];
-    const uint2 w = reinterpret_cast<const uint2*>(kv ? a.c.v_codes : a.c.k_codes)[((size_t)unit * a.c.capacity + p) * CH + c];
-    unsigned f[4], o[4];
-    codes_to_half4<FMT>(w.x, f[0], f[1]);
-    codes_to_half4<FMT>(w.y, f[2], f[3]);
+  const int whole = len / kQ8Block * kQ8Block;
+  const uint2* codes = reinterpret_cast<const uint2*>(kv ? a.c.v_codes : a.c.k_codes) + (size_t)unit * a.c.capacity * CH;
+  const uint4* ring = reinterpret_cast<const uint4*>(kv ? a.c.v_recent : a.c.k_recent) + (size_t)unit * kQ8Ring * CH;
+  const float* scales = (kv ? a.c.v_scales : a.c.k_scales) + (size_t)unit * (a.c.capacity / kQ8Block);
+  uint4* out = reinterpret_cast<uint4*>(a.out[kv]) + (size_t)unit * a.n * CH;
+  const int64_t i0 = (int64_t)blockIdx.x * kReadThreads * kReadItems + threadIdx.x;
+  uint4 x[kReadItems];                                     // codes in x, y and their scale in z, or 16-bit values
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 v = unpack16<__half>(f[e]);
-      o[e] = pack16<T>(__fmul_rn(v.x, s), __fmul_rn(v.y, s));
+  for (int j = 0; j < kReadItems; ++j) {
+    const int64_t i = i0 + j * kReadThreads, t = i / CH, p = a.start + t;
+    if (t >= a.n || p >= len) continue;
+    if (p >= whole) {
+      x[j] = ring[p % kQ8Ring * CH + i % CH];
+    } else {
+      const uint2 w = codes[p * CH + i % CH];
+      x[j] = make_uint4(w.x, w.y, __float_as_uint(scales[p / kQ8Block]), 0u);
     }
-    r = make_uint4(o[0], o[1], o[2], o[3]);
   }
-  reinterpret_cast<uint4*>(a.out[kv])[((size_t)unit * a.n + t) * CH + c] = r;
+#pragma unroll
+  for (int j = 0; j < kReadItems; ++j) {
+    const int64_t i = i0 + j * kReadThreads, t = i / CH, p = a.start + t;
+    if (t >= a.n || p >= len) continue;
+    if (p < whole) {
+      const float s = __uint_as_float(x[j].z);
+      unsigned f[4], o[4];
+      codes_to_half4<FMT>(x[j].x, f[0], f[1]);
+      codes_to_half4<FMT>(x[j].y, f[2], f[3]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 v = unpack16<__half>(f[e]);
+        o[e] = pack16<T>(__fmul_rn(v.x, s), __fmul_rn(v.y, s));
+      }
+      x[j] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    out[i] = x[j];
+  }
 }
 
 // ---- norm and rotation ------------------------------------------------------
-// One CTA per token: its angles' cosines and sines once (float64 reduction of
-// position x frequency to a turn, then a float32 sincos), then D / 16 lanes
-// per head, each with one 16-byte chunk of either half of the head, so that
-// both elements of every pair are in one lane in either layout of the pairs.
+// A CTA takes TOK tokens' heads, or part of them: the angles' cosines and
+// sines once per token (position x frequency reduced to a turn in float64,
+// then a float32 sincos), and D / 16 lanes per head, each with one 16-byte
+// chunk of either half of the head, so that both elements of every pair are
+// in one lane in either layout of the pairs.  A lane's next head is loaded
+// before the last one's is worked on, the first before the angles.
 constexpr int kRopeThreads = 256;
 
-template <typename T, int D>
+template <typename T, int D, int TOK>
 __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const NormRopeArgs a) {
-  constexpr int L = D / 16;                              // lanes per head
-  __shared__ float2 cs[D / 2];
-  const int64_t tok = blockIdx.x;
-  const int b = (int)(tok / a.n), t = (int)(tok % a.n), tid = threadIdx.x;
-  if (tid < D / 2) {
-    const double two_pi = 6.283185307179586476925286766559;
-    const double ang = (double)a.positions[tok] * (double)a.inv_freq[tid];
-    const float r = (float)(ang - two_pi * rint(ang / two_pi));
-    float s, c;
-    sincosf(r, &s, &c);
-    cs[tid] = make_float2(c, s);
+  constexpr int L = D / 16, GROUPS = kRopeThreads / L;     // lanes per head, heads at a time
+  __shared__ float2 cs[TOK][D / 2];
+  const int tid = threadIdx.x, lane = tid % L, H = a.Hq + a.Hkv;
+  const int64_t tok0 = (int64_t)blockIdx.x * TOK, tokens = (int64_t)a.batch * a.n;
+  const int count = (int)min((int64_t)TOK, tokens - tok0) * H;  // heads of this CTA's tokens
+  const int step = GROUPS * gridDim.y;
+  auto source = [&](int v) {
+    const int h = v % H;
+    const int64_t tok = tok0 + v / H, b = tok / a.n, t = tok % a.n;
+    return reinterpret_cast<const uint4*>(h < a.Hq ? static_cast<const T*>(a.q) + b * a.q_row + t * a.q_token + h * a.q_head
+                                                   : static_cast<const T*>(a.k) + b * a.k_row + t * a.k_token + (h - a.Hq) * a.k_head) + lane;
+  };
+  int v = blockIdx.y * GROUPS + tid / L;
+  uint4 next[2];
+  if (v < count) {
+    const uint4* src = source(v);
+    next[0] = src[0], next[1] = src[L];
+  }
+  for (int i = tid; i < TOK * (D / 2); i += kRopeThreads) {
+    if (tok0 + i / (D / 2) < tokens) {
+      const double turns = 0.15915494309189533577;         // 1 / (2 pi)
+      const double ang = (double)a.positions[tok0 + i / (D / 2)] * (double)a.inv_freq[i % (D / 2)];
+      const float r = (float)fma(-6.283185307179586476925286766559, rint(ang * turns), ang);
+      float s, c;
+      sincosf(r, &s, &c);
+      cs[i / (D / 2)][i % (D / 2)] = make_float2(c, s);
+    }
   }
   __syncthreads();
-  const int lane = tid % L;
-  for (int h0 = 0; h0 < a.Hq + a.Hkv; h0 += kRopeThreads / L) {
-    const int h = h0 + tid / L;
-    const bool on = h < a.Hq + a.Hkv, isq = h < a.Hq;
-    if (!on) break;                                      // whole groups of L lanes leave together
-    const int hh = isq ? h : h - a.Hq;
-    const T* src = isq ? static_cast<const T*>(a.q) + b * a.q_row + t * a.q_token + hh * a.q_head
-                       : static_cast<const T*>(a.k) + b * a.k_row + t * a.k_token + hh * a.k_head;
+  for (; v < count; v += step) {                           // whole groups of L lanes leave together
+    const uint4 cur[2] = {next[0], next[1]};
+    if (v + step < count) {
+      const uint4* src = source(v + step);
+      next[0] = src[0], next[1] = src[L];
+    }
+    const int h = v % H;
+    const int64_t tok = tok0 + v / H;
+    const bool isq = h < a.Hq;
     const void* wt = isq ? a.q_weight : a.k_weight;
     float x[16];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const uint4 v = reinterpret_cast<const uint4*>(src)[lane + e * L];
-      const unsigned w[4] = {v.x, v.y, v.z, v.w};
+      const unsigned w[4] = {cur[e].x, cur[e].y, cur[e].z, cur[e].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 f = unpack16<T>(w[i]);
@@ -201,7 +236,7 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const NormRopeA
       const unsigned mask = ((1u << L) - 1u) << (tid % 32 / L * L);
 #pragma unroll
       for (int o = L / 2; o; o /= 2) ss += __shfl_xor_sync(mask, ss, o);
-      float r = 1.0f / sqrtf(ss / D + a.eps);
+      const float r = 1.0f / sqrtf(ss / D + a.eps);
       // bf16 squares can leave float32 at either end: such heads take float64
       double rd = 0.0;
       const bool wide = Pair16<T>::kWide && !(ss > 1e-30f && ss < 1e38f);
@@ -215,8 +250,8 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const NormRopeA
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const uint4 v = reinterpret_cast<const uint4*>(wt)[lane + e * L];
-        const unsigned w[4] = {v.x, v.y, v.z, v.w};
+        const uint4 u = reinterpret_cast<const uint4*>(wt)[lane + e * L];
+        const unsigned w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 f = unpack16<T>(w[i]);
@@ -229,14 +264,15 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const NormRopeA
     float y[16];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int i0 = a.interleaved ? 2 * i : i, i1 = a.interleaved ? 2 * i + 1 : i + 8;
-      const int j = a.interleaved ? (i < 4 ? 4 * lane + i : D / 4 + 4 * lane + i - 4) : 8 * lane + i;
-      const float2 w = cs[j];
-      y[i0] = x[i0] * w.x - x[i1] * w.y;
-      y[i1] = x[i1] * w.x + x[i0] * w.y;
+      // the turn of pair i: elements i, i + 8 of the lane, or 2 i, 2 i + 1
+      const float2 w = cs[v / H][a.interleaved ? (i < 4 ? 4 * lane + i : D / 4 + 4 * lane + i - 4) : 8 * lane + i];
+      const float x0 = a.interleaved ? x[2 * i] : x[i], x1 = a.interleaved ? x[2 * i + 1] : x[i + 8];
+      const float y0 = x0 * w.x - x1 * w.y, y1 = x1 * w.x + x0 * w.y;
+      if (a.interleaved) y[2 * i] = y0, y[2 * i + 1] = y1;
+      else y[i] = y0, y[i + 8] = y1;
     }
-    T* dst = isq ? static_cast<T*>(a.q_out) + ((size_t)tok * a.Hq + hh) * D
-                 : static_cast<T*>(a.k_out) + (((size_t)b * a.Hkv + hh) * a.n + t) * D;
+    T* dst = isq ? static_cast<T*>(a.q_out) + ((size_t)tok * a.Hq + h) * D
+                 : static_cast<T*>(a.k_out) + (((size_t)(tok / a.n) * a.Hkv + h - a.Hq) * a.n + tok % a.n) * D;
 #pragma unroll
     for (int e = 0; e < 2; ++e)
       reinterpret_cast<uint4*>(dst)[lane + e * L] =
@@ -262,7 +298,8 @@ cudaError_t launch_q8_append(const Q8AppendArgs& a, cudaStream_t s) {
 
 cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s) {
   const int64_t chunks = (int64_t)a.n * (a.c.head_dim / 8);
-  const dim3 grid((unsigned)((chunks + kReadThreads - 1) / kReadThreads), (unsigned)(a.c.batch * a.c.num_kv_heads), 2);
+  const int per = kReadThreads * kReadItems;
+  const dim3 grid((unsigned)((chunks + per - 1) / per), (unsigned)(a.c.batch * a.c.num_kv_heads), 2);
   auto go = [&](auto fn) { fn<<<grid, kReadThreads, 0, s>>>(a); };
   const bool h = a.c.dtype == TQ_DTYPE_FP16, i8 = a.c.format == TQ_Q8_INT8;
 #define TQ_READ(D)                                                                              \
@@ -275,14 +312,20 @@ cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t s) {
-  const unsigned grid = (unsigned)((int64_t)a.batch * a.n);
+  const int64_t tokens = (int64_t)a.batch * a.n;
+  const int H = a.Hq + a.Hkv, groups = kRopeThreads / (a.d / 16);
+  // Few tokens: one each, their heads over several CTAs.  Many: four tokens a CTA, which share its start.
+  const bool many = tokens >= 4096;
+  const int tok = many ? 4 : 1;
+  const dim3 grid((unsigned)((tokens + tok - 1) / tok), many ? 1u : (unsigned)((H + groups - 1) / groups));
+  auto go = [&](auto fn) { fn<<<grid, kRopeThreads, 0, s>>>(a); };
   const bool h = a.dtype == TQ_DTYPE_FP16;
-  if (a.d == 64)
-    h ? norm_rope_kernel<__half, 64><<<grid, kRopeThreads, 0, s>>>(a)
-      : norm_rope_kernel<__nv_bfloat16, 64><<<grid, kRopeThreads, 0, s>>>(a);
-  else
-    h ? norm_rope_kernel<__half, 128><<<grid, kRopeThreads, 0, s>>>(a)
-      : norm_rope_kernel<__nv_bfloat16, 128><<<grid, kRopeThreads, 0, s>>>(a);
+#define TQ_ROPE(D)                                                                              \
+  h ? (many ? go(norm_rope_kernel<__half, D, 4>) : go(norm_rope_kernel<__half, D, 1>))          \
+    : (many ? go(norm_rope_kernel<__nv_bfloat16, D, 4>) : go(norm_rope_kernel<__nv_bfloat16, D, 1>))
+  if (a.d == 64) TQ_ROPE(64);
+  else TQ_ROPE(128);
+#undef TQ_ROPE
   return cudaGetLastError();
 }
 

@@ -15,6 +15,7 @@
 // latency, the open block's, the join of the warps).  A unit inside one CTA's
 // run is finished there; the others leave partial results that a second
 // kernel joins in a fixed order.
+#include <atomic>
 #include <cmath>
 
 #include "tq_q8.cuh"
@@ -23,8 +24,8 @@ namespace tq {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kStages = 3;
-constexpr int kUnitCost = 3;                 // of a unit besides its tiles, in tiles
+constexpr int kStages = 2;
+constexpr int kUnitCost = 8;                 // of a unit besides its tiles, in tiles
 constexpr int kMinPlaces = 4;                // that a CTA takes at least
 constexpr float kLowest = -3.0e38f;          // of a reference before its first token
 constexpr float kShift = 7.f;                // numerator weights are 2^7 at their reference (mv holds it less 7),
@@ -65,6 +66,7 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
@@ -141,12 +143,14 @@ __device__ __forceinline__ uint32_t plan_ctas(uint32_t places, uint32_t grid) {
   const uint32_t most = (places + kMinPlaces - 1) / kMinPlaces;
   return most < grid ? most : grid;
 }
+// Runs of places / ctas places, one more in the first ones.
 __device__ __forceinline__ uint32_t cta_start(uint32_t c, uint32_t places, uint32_t ctas) {
-  return (uint32_t)((uint64_t)c * places / ctas);
+  return c * (places / ctas) + min(c, places % ctas);
 }
 // The CTA whose run holds place t.
 __device__ __forceinline__ uint32_t cta_of(uint32_t t, uint32_t places, uint32_t ctas) {
-  return (uint32_t)((((uint64_t)t + 1) * ctas + places - 1) / places) - 1;
+  const uint32_t len = places / ctas, more = places % ctas, longer = more * (len + 1);
+  return t < longer ? t / (len + 1) : more + (t - longer) / len;
 }
 
 // A CTA's run, segment by segment: a segment is the run's tiles [begin, end) of one unit (kv head x query
@@ -587,6 +591,19 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q8_attend_kernel
       kp = static_cast<const uint8_t*>(a.c.k_codes) + at;
       vp = static_cast<const uint8_t*>(a.c.v_codes) + at;
       sp = (ps.lane ? a.c.v_scales : a.c.k_scales) + unit * (a.c.capacity / kQ8Block) + get->begin;
+      // What the pass reads outside the ring, into L2: behind the fetches in flight it would wait for them all.
+      if (ps.lane < S::ROWS)
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+          prefetch_l2(ps.q_row(a, get->row, get->sub / groups, get->sub % groups * S::ROWS + ps.lane) + 64 * i);
+      const int cnt = plan.len[get->row] - get->whole * kQ8Block - 16 * ps.warp;
+      if (get->end > get->whole && cnt > 0) {
+        const size_t open = (unit * kQ8Ring + (get->whole & 1) * kQ8Block + 16 * ps.warp) * D;
+        for (int i = ps.lane; i < min(cnt, 16) * (D / 64); i += 32) {
+          prefetch_l2(static_cast<const T*>(a.c.k_recent) + open + 64 * i);
+          prefetch_l2(static_cast<const T*>(a.c.v_recent) + open + 64 * i);
+        }
+      }
     }
     if (more > 0) {
 #pragma unroll
@@ -781,8 +798,17 @@ template <typename T, int FMT, int D, int NT>
 cudaError_t launch(const Q8AttendArgs& a, uint32_t grid, cudaStream_t s) {
   const int smem = smem_bytes<D, NT>(a.c.batch);
   auto kernel = q8_attend_kernel<T, FMT, D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // once per device: the most that any batch takes
+  static std::atomic<uint64_t> set{0};
+  int dev;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev % 64);
+  if (!(set.load(std::memory_order_relaxed) & bit) || dev >= 64) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D, NT>(kQ8MaxRows));
+    if (e != cudaSuccess) return e;
+    set.fetch_or(bit, std::memory_order_relaxed);
+  }
   kernel<<<grid, kThreads, smem, s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;

@@ -514,6 +514,16 @@ def _q8_dtypes():
     return {torch.float16: 0, torch.bfloat16: 1}
 
 
+def _raw_stream(torch, index: int, stream) -> int:
+    """The stream to launch on: ``stream``, or PyTorch's current one of the
+    device.  The device must be the current one (the library launches there)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device.index != index:
+        raise ValueError(f"expected a stream of cuda:{index}")
+    return stream.cuda_stream
+
+
 class TQ8Cache:
     """A layer's KV cache in 8 bits: whole blocks of 64 tokens as int8 or e4m3
     codes with one float32 scale per (row, kv head, block), the open block in a
@@ -533,6 +543,7 @@ class TQ8Cache:
     def __init__(self, batch, num_kv_heads, head_dim, capacity, format="int8", dtype=None,
                  device="cuda", buffers=None):
         import torch
+        self._torch = torch
         dtype = torch.float16 if dtype is None else dtype
         if format not in self.FORMATS:
             raise ValueError("format is 'int8' or 'e4m3'")
@@ -560,128 +571,151 @@ class TQ8Cache:
                                   _ptr(self.v_scales), _ptr(self.k_recent), _ptr(self.v_recent),
                                   _ptr(self.status))
         self._ref = ctypes.addressof(self.struct)
-        self._scratch_bytes = {}
+        self._lib = lib()
+        self._index = device.index if device.type == "cuda" else -1
         self._shape = (batch, num_kv_heads, head_dim)
+        self._scratch_size, self._scratch = {}, {}
         # the sizes are checked here once, by the library (no device call)
-        _check(lib().tq_q8_append(self._ref, None, None, 0, 0, 0, 0, 0, 0, 0, None, None, None), "TQ8Cache")
+        _check(self._lib.tq_q8_append(self._ref, None, None, 0, 0, 0, 0, 0, 0, 0, None, None, None), "TQ8Cache")
 
-    def _guard(self):
-        """The cache's device as the current one (the library launches there)."""
-        import torch
-        return torch.cuda.device(self.device)
+    def _on_device(self, method, *args):
+        with self._torch.cuda.device(self.device):
+            return method(*args)
 
-    def _stream(self, stream):
-        import torch
-        if stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
-        if stream.device != self.device:
-            raise ValueError(f"expected a stream of {self.device}")
-        return stream.cuda_stream
+    def _elsewhere(self):
+        """Whether another device is the current one: the library launches there."""
+        return self._index >= 0 and self._torch._C._cuda_getDevice() != self._index
 
     def _ints(self, t, what):
-        import torch
-        if t is None:
-            return None
-        if t.dtype != torch.int32 or t.device != self.device or t.dim() != 1 or t.shape[0] != self._shape[0] \
+        if t.dtype is not self._torch.int32 or t.get_device() != self._index or t.shape != self._shape[:1] \
                 or not t.is_contiguous():
             raise ValueError(f"{what}: expected a contiguous int32 [{self._shape[0]}] on {self.device}")
         return t.data_ptr()
 
-    def _values(self, t, what, dims):
-        if t.dtype != self.dtype or t.device != self.device or t.dim() != dims:
-            raise ValueError(f"{what}: expected {self.dtype} with {dims} dimensions on {self.device}")
-        if t.stride(-1) != 1:
+    def _values(self, t, what):
+        if t.dtype is not self.dtype or t.get_device() != self._index:
+            raise ValueError(f"{what}: expected {self.dtype} on {self.device}")
+        s = t.stride()
+        if s[-1] != 1:
             raise ValueError(f"{what}: the head dimension must be contiguous")
-        return t.data_ptr()
+        return t.data_ptr(), s
 
     def append(self, k, v, lens, n_rows=None, stream=None):
         """k, v [B, Hkv, n, d] (any strides with d contiguous) become tokens
         lens[b] .. lens[b] + n_rows[b] - 1 of row b (n_rows None: n each)."""
         b, h, d = self._shape
-        n = k.shape[2] if k.dim() == 4 else -1
-        if tuple(k.shape) != (b, h, n, d) or k.shape != v.shape:
+        shape = k.shape
+        if len(shape) != 4 or shape[0] != b or shape[1] != h or shape[3] != d or v.shape != shape:
             raise ValueError(f"k, v: expected [{b}, {h}, n, {d}]")
-        kp, vp = self._values(k, "k", 4), self._values(v, "v", 4)
-        ks, vs = k.stride(), v.stride()
-        lp, rp = self._ints(lens, "lens"), self._ints(n_rows, "n_rows")
-        with self._guard():
-            code = lib().tq_q8_append(self._ref, kp, vp, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], n, lp, rp,
-                                      self._stream(stream))
-        _check(code, "tq_q8_append")
+        kp, ks = self._values(k, "k")
+        vp, vs = self._values(v, "v")
+        lp = self._ints(lens, "lens")
+        rp = None if n_rows is None else self._ints(n_rows, "n_rows")
+        if self._elsewhere():
+            return self._on_device(self.append, k, v, lens, n_rows, stream)
+        code = self._lib.tq_q8_append(self._ref, kp, vp, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], shape[2], lp, rp,
+                                      _raw_stream(self._torch, self._index, stream))
+        if code:
+            _check(code, "tq_q8_append")
 
     def read(self, lens, start=0, n=None, out=None, stream=None):
         """Positions start .. start + n - 1 of every row as 16-bit K, V
         [B, Hkv, n, d].  ``out``: a pair to write into, whose values that belong
         to no token stay; without it they are zero."""
-        import torch
         b, h, d = self._shape
         if out is None:
             if n is None:
                 raise ValueError("read needs n or out")
-            out = tuple(torch.zeros((b, h, n, d), dtype=self.dtype, device=self.device) for _ in "kv")
+            if stream is not None:                       # what is allocated here belongs to the call's stream
+                with self._torch.cuda.stream(stream):
+                    return self.read(lens, start, n)
+            out = tuple(self._torch.zeros((b, h, n, d), dtype=self.dtype, device=self.device) for _ in "kv")
         ko, vo = out
-        n = ko.shape[2] if n is None and ko.dim() == 4 else n
-        for t in out:
-            if tuple(t.shape) != (b, h, n, d) or t.dtype != self.dtype or t.device != self.device \
-                    or not t.is_contiguous():
-                raise ValueError(f"out: expected two contiguous {self.dtype} [{b}, {h}, {n}, {d}] on {self.device}")
+        shape = ko.shape
+        if len(shape) != 4 or shape[0] != b or shape[1] != h or shape[3] != d or vo.shape != shape \
+                or (n is not None and n != shape[2]) or not ko.is_contiguous() or not vo.is_contiguous():
+            raise ValueError(f"out: expected two contiguous [{b}, {h}, n, {d}]")
+        kp, vp = self._values(ko, "out")[0], self._values(vo, "out")[0]
         lp = self._ints(lens, "lens")
-        with self._guard():
-            code = lib().tq_q8_read(self._ref, lp, start, n, ko.data_ptr(), vo.data_ptr(), self._stream(stream))
-        _check(code, "tq_q8_read")
+        if self._elsewhere():
+            return self._on_device(self.read, lens, start, n, out, stream)
+        code = self._lib.tq_q8_read(self._ref, lp, start, shape[2], kp, vp,
+                                    _raw_stream(self._torch, self._index, stream))
+        if code:
+            _check(code, "tq_q8_read")
         return out
 
     def scratch_bytes(self, num_q_heads, n):
         """Bytes of scratch of an attention call (as tq_q8_attention_bytes)."""
         key = (num_q_heads, n)
-        if key not in self._scratch_bytes:
-            size = c_size_t()
-            with self._guard():
-                code = lib().tq_q8_attention_bytes(self._ref, num_q_heads, n, ctypes.byref(size))
-            _check(code, "tq_q8_attention_bytes")
-            self._scratch_bytes[key] = size.value
-        return self._scratch_bytes[key]
+        size = self._scratch_size.get(key)
+        if size is None:
+            if self._elsewhere():
+                return self._on_device(self.scratch_bytes, num_q_heads, n)
+            got = c_size_t()
+            _check(self._lib.tq_q8_attention_bytes(self._ref, num_q_heads, n, ctypes.byref(got)),
+                   "tq_q8_attention_bytes")
+            size = self._scratch_size[key] = got.value
+        return size
+
+    def _take_scratch(self, size, raw):
+        """Scratch of the call: one buffer per stream, whose calls follow one
+        another; a captured call gets its own, from its graph's memory, since
+        graphs may be replayed beside anything."""
+        torch = self._torch
+        if torch._C._cuda_isCurrentStreamCapturing():
+            return torch.empty(size, dtype=torch.uint8, device=self.device)
+        t = self._scratch.get(raw)
+        if t is None or t.shape[0] < size:
+            t = self._scratch[raw] = torch.empty(size, dtype=torch.uint8, device=self.device)
+        return t
 
     def attention(self, q, lens, n_rows=None, out=None, softmax_scale=0.0, scratch=None, stream=None):
         """q [B, n, Hq, d] (or [B, Hq, d] for one token): the newest n tokens'
         queries, attending to their row's positions up to their own; lens
         counts them.  Returns ``out`` in q's shape and type.  ``scratch``: a
-        uint8 tensor of scratch_bytes; without it one is taken from PyTorch's
-        allocator for the call."""
-        import torch
-        b, h, d = self._shape
-        one = q.dim() == 3
-        n = 1 if one else q.shape[1]
-        hq = q.shape[-2]
-        qp = self._values(q, "q", 3 if one else 4)
-        if q.shape[0] != b or q.shape[-1] != d:
-            raise ValueError(f"q: expected [{b}, n, Hq, {d}]")
-        qs = q.stride()
-        lp, rp = self._ints(lens, "lens"), self._ints(n_rows, "n_rows")
-        size = self.scratch_bytes(hq, n)
-        if stream is not None and (out is None or scratch is None):
-            # what is allocated here belongs to the stream of the call
+        uint8 tensor of scratch_bytes for the call (without it the object's)."""
+        torch = self._torch
+        if stream is not None:                           # what is allocated here belongs to the call's stream
+            if stream.device != self.device:
+                raise ValueError(f"expected a stream of {self.device}")
             with torch.cuda.stream(stream):
                 return self.attention(q, lens, n_rows, out, softmax_scale, scratch)
+        b, h, d = self._shape
+        shape = q.shape
+        dims = len(shape)
+        if not 3 <= dims <= 4 or shape[0] != b or shape[-1] != d:
+            raise ValueError(f"q: expected [{b}, n, Hq, {d}]")
+        n, hq = (shape[1], shape[2]) if dims == 4 else (1, shape[1])
+        qp, qs = self._values(q, "q")
+        lp = self._ints(lens, "lens")
+        rp = None if n_rows is None else self._ints(n_rows, "n_rows")
+        if self._elsewhere():
+            return self._on_device(self.attention, q, lens, n_rows, out, softmax_scale, scratch)
+        raw = torch._C._cuda_getCurrentRawStream(self._index)
+        size = self._scratch_size.get((hq, n))
+        if size is None:
+            size = self.scratch_bytes(hq, n)
         if out is None:
-            out = torch.empty(q.shape, dtype=self.dtype, device=self.device)
-        elif out.shape != q.shape or out.dtype != self.dtype or out.device != self.device or not out.is_contiguous():
+            out = torch.empty(shape, dtype=self.dtype, device=self.device)
+        elif out.shape != shape or out.dtype is not self.dtype or out.get_device() != self._index \
+                or not out.is_contiguous():
             raise ValueError("out: expected a contiguous tensor of q's shape and type")
         if scratch is None:
-            scratch = torch.empty(size, dtype=torch.uint8, device=self.device)
-        elif scratch.dtype != torch.uint8 or scratch.device != self.device or not scratch.is_contiguous():
+            scratch = self._take_scratch(size, raw)
+        elif scratch.dtype is not torch.uint8 or scratch.get_device() != self._index or not scratch.is_contiguous():
             raise ValueError(f"scratch: expected a contiguous uint8 tensor on {self.device}")
-        with self._guard():
-            code = lib().tq_q8_attention(self._ref, qp, qs[0], 0 if one else qs[1], qs[-2], hq, n, lp, rp,
-                                         softmax_scale, out.data_ptr(), scratch.data_ptr(), scratch.numel(),
-                                         self._stream(stream))
-        _check(code, "tq_q8_attention")
+        code = self._lib.tq_q8_attention(self._ref, qp, qs[0], qs[1] if dims == 4 else 0, qs[-2], hq, n, lp, rp,
+                                         softmax_scale, out.data_ptr(), scratch.data_ptr(), scratch.shape[0], raw)
+        if code:
+            _check(code, "tq_q8_attention")
         return out
 
     def get_status(self, stream=None):
         """Latched device status (0 = TQ_OK); waits for the stream, then clears it."""
-        with self._guard():
-            return lib().tq_q8_get_status(self._ref, self._stream(stream))
+        if self._elsewhere():
+            return self._on_device(self.get_status, stream)
+        return self._lib.tq_q8_get_status(self._ref, _raw_stream(self._torch, self._index, stream))
 
 
 def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
@@ -692,38 +726,42 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e
     inv_freq float32 [d / 2].  Returns q_out [B, n, Hq, d] and k_out
     [B, Hkv, n, d], the layouts that the caches' calls take."""
     import torch
-    if q.dim() != 4 or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
+    if stream is not None:                               # what is allocated here belongs to the call's stream
+        if stream.device != q.device:
+            raise ValueError(f"expected a stream of {q.device}")
+        with torch.cuda.stream(stream):
+            return qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, q_out, k_out)
+    if q.dim() != 4 or k.dim() != 4:
         raise ValueError("expected q [B, n, Hq, d] and k [B, n, Hkv, d]")
     b, n, hq, d = q.shape
-    hk, dev, dtype = k.shape[2], q.device, q.dtype
-    if dtype not in _q8_dtypes() or k.dtype != dtype or not q.is_cuda or k.device != dev:
-        raise ValueError("q, k: expected CUDA float16 or bfloat16 tensors of one type and device")
-    if (d > 1 and q.numel() and q.stride(3) != 1) or (d > 1 and k.numel() and k.stride(3) != 1):
+    b2, n2, hk, d2 = k.shape
+    index, dtype = q.get_device(), q.dtype
+    code = 0 if dtype is torch.float16 else 1 if dtype is torch.bfloat16 else -1
+    if b != b2 or n != n2 or d != d2 or code < 0 or k.dtype is not dtype or index < 0 or k.get_device() != index:
+        raise ValueError("expected q [B, n, Hq, d] and k [B, n, Hkv, d], CUDA float16 or bfloat16 of one type and device")
+    qs, ks = q.stride(), k.stride()
+    if (qs[3] != 1 and q.numel()) or (ks[3] != 1 and k.numel()):
         raise ValueError("q, k: the head dimension must be contiguous")
+    if q_out is None:
+        q_out = torch.empty((b, n, hq, d), dtype=dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty((b, hk, n, d), dtype=dtype, device=q.device)
     for t, what, shape, dt in ((positions, "positions", (b, n), torch.int32), (inv_freq, "inv_freq", (d // 2,), torch.float32),
                                (q_weight, "q_weight", (d,), dtype), (k_weight, "k_weight", (d,), dtype),
                                (q_out, "q_out", (b, n, hq, d), dtype), (k_out, "k_out", (b, hk, n, d), dtype)):
         if t is None:
             if what in ("positions", "inv_freq"):
                 raise ValueError(f"{what} is needed")
-        elif tuple(t.shape) != shape or t.dtype != dt or t.device != dev or not t.is_contiguous():
-            raise ValueError(f"{what}: expected a contiguous {dt} {list(shape)} on {dev}")
-    if stream is not None and (q_out is None or k_out is None):
-        with torch.cuda.stream(stream):
+        elif t.shape != shape or t.dtype is not dt or t.get_device() != index or not t.is_contiguous():
+            raise ValueError(f"{what}: expected a contiguous {dt} {list(shape)} on cuda:{index}")
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
             return qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, q_out, k_out)
-    if q_out is None:
-        q_out = torch.empty((b, n, hq, d), dtype=dtype, device=dev)
-    if k_out is None:
-        k_out = torch.empty((b, hk, n, d), dtype=dtype, device=dev)
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"expected a stream of {dev}")
-    s = (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
-    qs, ks = q.stride(), k.stride()
-    with torch.cuda.device(dev):
-        code = lib().tq_qk_norm_rope(b, n, hq, hk, d, _q8_dtypes()[dtype], q.data_ptr(), qs[0], qs[1], qs[2],
-                                     k.data_ptr(), ks[0], ks[1], ks[2], positions.data_ptr(), inv_freq.data_ptr(),
-                                     None if q_weight is None else q_weight.data_ptr(),
-                                     None if k_weight is None else k_weight.data_ptr(), eps, int(interleaved),
-                                     q_out.data_ptr(), k_out.data_ptr(), s)
-    _check(code, "tq_qk_norm_rope")
+    code = lib().tq_qk_norm_rope(b, n, hq, hk, d, code, q.data_ptr(), qs[0], qs[1], qs[2], k.data_ptr(), ks[0],
+                                 ks[1], ks[2], positions.data_ptr(), inv_freq.data_ptr(),
+                                 None if q_weight is None else q_weight.data_ptr(),
+                                 None if k_weight is None else k_weight.data_ptr(), eps, 1 if interleaved else 0,
+                                 q_out.data_ptr(), k_out.data_ptr(), torch._C._cuda_getCurrentRawStream(index))
+    if code:
+        _check(code, "tq_qk_norm_rope")
     return q_out, k_out
