@@ -53,10 +53,18 @@ __global__ void __launch_bounds__(kAppendThreads) q8_append_kernel(const Q8Appen
   if ((blk + 1) * kQ8Block <= end) {
     uint4 x[ITEMS];
     unsigned mx = 0;                                     // magnitudes' bits, two 16-bit lanes
+    constexpr int TOKS = kAppendThreads / CH;            // tokens at a time
+    const int p0 = blk * kQ8Block + tid / CH, c = tid % CH;
+    const uint4* src = in + (int64_t)(p0 - len) * tstride + c;
+    if (blk * kQ8Block >= len) {
 #pragma unroll
-    for (int j = 0; j < ITEMS; ++j) {
-      const int i = tid + j * kAppendThreads, p = blk * kQ8Block + i / CH, c = i % CH;
-      x[j] = p < len ? ring[(p % kQ8Ring) * CH + c] : in[(int64_t)(p - len) * tstride + c];
+      for (int j = 0; j < ITEMS; ++j) x[j] = src[j * TOKS * tstride];
+    } else {
+#pragma unroll
+      for (int j = 0; j < ITEMS; ++j) {
+        const int p = p0 + j * TOKS;
+        x[j] = p < len ? ring[(p % kQ8Ring) * CH + c] : src[j * TOKS * tstride];
+      }
     }
 #pragma unroll
     for (int j = 0; j < ITEMS; ++j) {
@@ -75,6 +83,10 @@ __global__ void __launch_bounds__(kAppendThreads) q8_append_kernel(const Q8Appen
     const float inv = live ? __fdiv_rn(q8_top<FMT>(), amax) : 0.f;
     uint2* codes = reinterpret_cast<uint2*>(kv ? a.c.v_codes : a.c.k_codes) +
                    ((size_t)unit * a.c.capacity + (size_t)blk * kQ8Block) * CH;
+    if (bad) {                                           // 0 * NaN would leave a NaN code
+#pragma unroll
+      for (int j = 0; j < ITEMS; ++j) x[j] = make_uint4(0u, 0u, 0u, 0u);
+    }
 #pragma unroll
     for (int j = 0; j < ITEMS; ++j) {
       const unsigned w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
@@ -82,7 +94,6 @@ __global__ void __launch_bounds__(kAppendThreads) q8_append_kernel(const Q8Appen
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float2 lo = unpack16<T>(w[2 * e]), hi = unpack16<T>(w[2 * e + 1]);
-        if (!live) lo = hi = make_float2(0.f, 0.f);      // 0 * NaN would leave a NaN code
         lo.x = __fmul_rn(lo.x, inv), lo.y = __fmul_rn(lo.y, inv);
         hi.x = __fmul_rn(hi.x, inv), hi.y = __fmul_rn(hi.y, inv);
         if (FMT == TQ_Q8_E4M3) {
@@ -135,24 +146,23 @@ __global__ void __launch_bounds__(kReadThreads) q8_read_kernel(const Q8ReadArgs 
   const uint2* codes = reinterpret_cast<const uint2*>(kv ? a.c.v_codes : a.c.k_codes) + (size_t)unit * a.c.capacity * CH;
   const uint4* ring = reinterpret_cast<const uint4*>(kv ? a.c.v_recent : a.c.k_recent) + (size_t)unit * kQ8Ring * CH;
   const float* scales = (kv ? a.c.v_scales : a.c.k_scales) + (size_t)unit * (a.c.capacity / kQ8Block);
-  uint4* out = reinterpret_cast<uint4*>(a.out[kv]) + (size_t)unit * a.n * CH;
+  uint4* out = reinterpret_cast<uint4*>(kv ? a.out[1] : a.out[0]) + (size_t)unit * a.n * CH;
   const int64_t i0 = (int64_t)blockIdx.x * kReadThreads * kReadItems + threadIdx.x;
   uint4 x[kReadItems];                                     // codes in x, y and their scale in z, or 16-bit values
 #pragma unroll
   for (int j = 0; j < kReadItems; ++j) {
     const int64_t i = i0 + j * kReadThreads, t = i / CH, p = a.start + t;
-    if (t >= a.n || p >= len) continue;
-    if (p >= whole) {
-      x[j] = ring[p % kQ8Ring * CH + i % CH];
-    } else {
+    x[j] = make_uint4(0u, 0u, 0u, 0u);
+    if (t < a.n && p < whole) {
       const uint2 w = codes[p * CH + i % CH];
-      x[j] = make_uint4(w.x, w.y, __float_as_uint(scales[p / kQ8Block]), 0u);
+      x[j].x = w.x, x[j].y = w.y, x[j].z = __float_as_uint(scales[p / kQ8Block]);
+    } else if (t < a.n && p < len) {
+      x[j] = ring[p % kQ8Ring * CH + i % CH];
     }
   }
 #pragma unroll
   for (int j = 0; j < kReadItems; ++j) {
     const int64_t i = i0 + j * kReadThreads, t = i / CH, p = a.start + t;
-    if (t >= a.n || p >= len) continue;
     if (p < whole) {
       const float s = __uint_as_float(x[j].z);
       unsigned f[4], o[4];
@@ -165,60 +175,70 @@ __global__ void __launch_bounds__(kReadThreads) q8_read_kernel(const Q8ReadArgs 
       }
       x[j] = make_uint4(o[0], o[1], o[2], o[3]);
     }
-    out[i] = x[j];
+    if (t < a.n && p < len) out[i] = x[j];
   }
 }
 
 // ---- norm and rotation ------------------------------------------------------
-// A CTA takes TOK tokens' heads, or part of them: the angles' cosines and
+// A CTA's warps take 8 / WPT tokens, WPT warps each: the angles' cosines and
 // sines once per token (position x frequency reduced to a turn in float64,
-// then a float32 sincos), and D / 16 lanes per head, each with one 16-byte
+// then a float32 sincos), then D / 16 lanes per head, each with one 16-byte
 // chunk of either half of the head, so that both elements of every pair are
-// in one lane in either layout of the pairs.  A lane's next head is loaded
-// before the last one's is worked on, the first before the angles.
+// in one lane in either layout of the pairs.  A lane keeps its pairs' turns
+// and its weights for all of its heads; its next head is loaded before the
+// last one's is worked on, the first before the angles.
 constexpr int kRopeThreads = 256;
 
-template <typename T, int D, int TOK>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const NormRopeArgs a) {
-  constexpr int L = D / 16, GROUPS = kRopeThreads / L;     // lanes per head, heads at a time
-  __shared__ float2 cs[TOK][D / 2];
-  const int tid = threadIdx.x, lane = tid % L, H = a.Hq + a.Hkv;
-  const int64_t tok0 = (int64_t)blockIdx.x * TOK, tokens = (int64_t)a.batch * a.n;
-  const int count = (int)min((int64_t)TOK, tokens - tok0) * H;  // heads of this CTA's tokens
-  const int step = GROUPS * gridDim.y;
-  auto source = [&](int v) {
-    const int h = v % H;
-    const int64_t tok = tok0 + v / H, b = tok / a.n, t = tok % a.n;
-    return reinterpret_cast<const uint4*>(h < a.Hq ? static_cast<const T*>(a.q) + b * a.q_row + t * a.q_token + h * a.q_head
-                                                   : static_cast<const T*>(a.k) + b * a.k_row + t * a.k_token + (h - a.Hq) * a.k_head) + lane;
+template <typename T, int D, int WPT, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads, 3) norm_rope_kernel(const NormRopeArgs a) {
+  constexpr int L = D / 16, HW = 32 / L, TOK = kRopeThreads / 32 / WPT;  // lanes per head, heads per warp, tokens
+  __shared__ float2 cs[TOK][D / 2];                        // a lane's i-th turn at [i L + lane]
+  const int tid = threadIdx.x, lane = tid % L, warp = tid / 32;
+  const int tok0 = (int)blockIdx.x * TOK, tokens = a.batch * a.n, tok = tok0 + warp / WPT;
+  const int step = HW * WPT * (int)gridDim.y;
+  const int b = tok / a.n, t = tok % a.n;
+  // The lane's next head: of the queries first, then of the keys.
+  bool keys = false;
+  int h = ((int)blockIdx.y * WPT + warp % WPT) * HW + tid % 32 / L, heads = a.Hq;
+  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + b * a.q_row + t * a.q_token + h * a.q_head) + lane;
+  auto settle = [&]() {                                    // from behind the queries to the keys
+    if (!keys && h >= a.Hq) {
+      keys = true, h -= a.Hq, heads = a.Hkv;
+      src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.k) + b * a.k_row + t * a.k_token + h * a.k_head) + lane;
+    }
   };
-  int v = blockIdx.y * GROUPS + tid / L;
-  uint4 next[2];
-  if (v < count) {
-    const uint4* src = source(v);
-    next[0] = src[0], next[1] = src[L];
-  }
+  if (tok >= tokens) h = a.Hq + a.Hkv;
+  settle();
+  uint4 next[2], wt[2];
+  if (h < heads) next[0] = src[0], next[1] = src[L];
   for (int i = tid; i < TOK * (D / 2); i += kRopeThreads) {
-    if (tok0 + i / (D / 2) < tokens) {
+    const int u = i / (D / 2), p = i % (D / 2);
+    if (tok0 + u < tokens) {
       const double turns = 0.15915494309189533577;         // 1 / (2 pi)
-      const double ang = (double)a.positions[tok0 + i / (D / 2)] * (double)a.inv_freq[i % (D / 2)];
+      const double ang = (double)a.positions[tok0 + u] * (double)a.inv_freq[p];
       const float r = (float)fma(-6.283185307179586476925286766559, rint(ang * turns), ang);
       float s, c;
       sincosf(r, &s, &c);
-      cs[i / (D / 2)][i % (D / 2)] = make_float2(c, s);
+      cs[u][INTER ? (p % 4 + p / (D / 4) * 4) * L + p % (D / 4) / 4 : p % 8 * L + p / 8] = make_float2(c, s);
     }
   }
   __syncthreads();
-  for (; v < count; v += step) {                           // whole groups of L lanes leave together
+  float2 turn[8];                                          // of the lane's pairs: elements i, i + 8, or 2 i, 2 i + 1
+#pragma unroll
+  for (int i = 0; i < 8; ++i) turn[i] = cs[warp / WPT][i * L + lane];
+  const T* weight = nullptr;                               // whose values wt holds
+  while (h < heads) {                                      // whole groups of L lanes leave together
     const uint4 cur[2] = {next[0], next[1]};
-    if (v + step < count) {
-      const uint4* src = source(v + step);
-      next[0] = src[0], next[1] = src[L];
+    uint4* dst = reinterpret_cast<uint4*>(keys ? static_cast<T*>(a.k_out) + (((size_t)b * a.Hkv + h) * a.n + t) * D
+                                               : static_cast<T*>(a.q_out) + ((size_t)tok * a.Hq + h) * D) + lane;
+    const T* own = static_cast<const T*>(keys ? a.k_weight : a.q_weight);
+    h += step, src += step * (keys ? a.k_head : a.q_head) / 8;
+    settle();
+    if (h < heads) next[0] = src[0], next[1] = src[L];
+    if (own != weight) {
+      weight = own;
+      if (own) wt[0] = reinterpret_cast<const uint4*>(own)[lane], wt[1] = reinterpret_cast<const uint4*>(own)[lane + L];
     }
-    const int h = v % H;
-    const int64_t tok = tok0 + v / H;
-    const bool isq = h < a.Hq;
-    const void* wt = isq ? a.q_weight : a.k_weight;
     float x[16];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -229,55 +249,51 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const NormRopeA
         x[8 * e + 2 * i] = f.x, x[8 * e + 2 * i + 1] = f.y;
       }
     }
-    if (wt) {
+    if (weight) {
       float ss = 0.f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
       const unsigned mask = ((1u << L) - 1u) << (tid % 32 / L * L);
 #pragma unroll
       for (int o = L / 2; o; o /= 2) ss += __shfl_xor_sync(mask, ss, o);
-      const float r = 1.0f / sqrtf(ss / D + a.eps);
-      // bf16 squares can leave float32 at either end: such heads take float64
-      double rd = 0.0;
-      const bool wide = Pair16<T>::kWide && !(ss > 1e-30f && ss < 1e38f);
-      if (wide) {
+      if (Pair16<T>::kWide && !(ss > 1e-30f && ss < 1e38f)) {
+        // bf16 squares can leave float32 at either end: such heads take float64
         double sd = 0.0;
 #pragma unroll
         for (int i = 0; i < 16; ++i) sd += (double)x[i] * x[i];
 #pragma unroll
         for (int o = L / 2; o; o /= 2) sd += __shfl_xor_sync(mask, sd, o);
-        rd = 1.0 / sqrt(sd / D + a.eps);
+        // in two factors, since the whole one may be no float32
+        const double rd = 1.0 / sqrt(sd / D + a.eps), half = rd > 1.0 ? 1.8446744073709552e19 : 5.421010862427522e-20;
+        const float r0 = (float)half, r1 = (float)(rd / half);   // 2^64 or 2^-64, and the rest
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = x[i] * r0 * r1;
+      } else {
+        const float r = rsqrtf(fmaf(ss, 1.0f / D, a.eps));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] *= r;
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const uint4 u = reinterpret_cast<const uint4*>(wt)[lane + e * L];
-        const unsigned w[4] = {u.x, u.y, u.z, u.w};
+        const unsigned w[4] = {wt[e].x, wt[e].y, wt[e].z, wt[e].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 f = unpack16<T>(w[i]);
-          float &x0 = x[8 * e + 2 * i], &x1 = x[8 * e + 2 * i + 1];
-          x0 = wide ? (float)(x0 * rd * f.x) : x0 * (r * f.x);
-          x1 = wide ? (float)(x1 * rd * f.y) : x1 * (r * f.y);
+          x[8 * e + 2 * i] *= f.x, x[8 * e + 2 * i + 1] *= f.y;
         }
       }
     }
     float y[16];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      // the turn of pair i: elements i, i + 8 of the lane, or 2 i, 2 i + 1
-      const float2 w = cs[v / H][a.interleaved ? (i < 4 ? 4 * lane + i : D / 4 + 4 * lane + i - 4) : 8 * lane + i];
-      const float x0 = a.interleaved ? x[2 * i] : x[i], x1 = a.interleaved ? x[2 * i + 1] : x[i + 8];
-      const float y0 = x0 * w.x - x1 * w.y, y1 = x1 * w.x + x0 * w.y;
-      if (a.interleaved) y[2 * i] = y0, y[2 * i + 1] = y1;
-      else y[i] = y0, y[i + 8] = y1;
+      constexpr int S = INTER ? 2 : 1, O = INTER ? 1 : 8;
+      y[S * i] = x[S * i] * turn[i].x - x[S * i + O] * turn[i].y;
+      y[S * i + O] = x[S * i + O] * turn[i].x + x[S * i] * turn[i].y;
     }
-    T* dst = isq ? static_cast<T*>(a.q_out) + ((size_t)tok * a.Hq + h) * D
-                 : static_cast<T*>(a.k_out) + (((size_t)(tok / a.n) * a.Hkv + h - a.Hq) * a.n + tok % a.n) * D;
 #pragma unroll
     for (int e = 0; e < 2; ++e)
-      reinterpret_cast<uint4*>(dst)[lane + e * L] =
-          make_uint4(pack16<T>(y[8 * e], y[8 * e + 1]), pack16<T>(y[8 * e + 2], y[8 * e + 3]),
-                     pack16<T>(y[8 * e + 4], y[8 * e + 5]), pack16<T>(y[8 * e + 6], y[8 * e + 7]));
+      dst[e * L] = make_uint4(pack16<T>(y[8 * e], y[8 * e + 1]), pack16<T>(y[8 * e + 2], y[8 * e + 3]),
+                                     pack16<T>(y[8 * e + 4], y[8 * e + 5]), pack16<T>(y[8 * e + 6], y[8 * e + 7]));
   }
 }
 
@@ -311,22 +327,22 @@ cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t s) {
-  const int64_t tokens = (int64_t)a.batch * a.n;
-  const int H = a.Hq + a.Hkv, groups = kRopeThreads / (a.d / 16);
-  // Few tokens: one each, their heads over several CTAs.  Many: four tokens a CTA, which share its start.
+template <typename T, int D>
+static cudaError_t launch_rope(const NormRopeArgs& a, cudaStream_t s) {
+  const int tokens = a.batch * a.n, heads = a.Hq + a.Hkv, at_once = 8 * (32 / (D / 16));
+  // Few tokens: eight warps each, their heads over several CTAs.  Many: two warps each, which keep a token's
+  // turns and the weights for all of its heads.
   const bool many = tokens >= 4096;
-  const int tok = many ? 4 : 1;
-  const dim3 grid((unsigned)((tokens + tok - 1) / tok), many ? 1u : (unsigned)((H + groups - 1) / groups));
+  const dim3 grid(many ? (tokens + 3) / 4 : tokens, many ? 1 : (heads + at_once - 1) / at_once);
   auto go = [&](auto fn) { fn<<<grid, kRopeThreads, 0, s>>>(a); };
-  const bool h = a.dtype == TQ_DTYPE_FP16;
-#define TQ_ROPE(D)                                                                              \
-  h ? (many ? go(norm_rope_kernel<__half, D, 4>) : go(norm_rope_kernel<__half, D, 1>))          \
-    : (many ? go(norm_rope_kernel<__nv_bfloat16, D, 4>) : go(norm_rope_kernel<__nv_bfloat16, D, 1>))
-  if (a.d == 64) TQ_ROPE(64);
-  else TQ_ROPE(128);
-#undef TQ_ROPE
+  if (a.interleaved) many ? go(norm_rope_kernel<T, D, 2, true>) : go(norm_rope_kernel<T, D, 8, true>);
+  else many ? go(norm_rope_kernel<T, D, 2, false>) : go(norm_rope_kernel<T, D, 8, false>);
   return cudaGetLastError();
+}
+
+cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t s) {
+  if (a.dtype == TQ_DTYPE_FP16) return a.d == 64 ? launch_rope<__half, 64>(a, s) : launch_rope<__half, 128>(a, s);
+  return a.d == 64 ? launch_rope<__nv_bfloat16, 64>(a, s) : launch_rope<__nv_bfloat16, 128>(a, s);
 }
 
 }  // namespace tq
