@@ -180,65 +180,87 @@ __global__ void __launch_bounds__(kReadThreads) q8_read_kernel(const Q8ReadArgs 
 }
 
 // ---- norm and rotation ------------------------------------------------------
-// A CTA's warps take 8 / WPT tokens, WPT warps each: the angles' cosines and
-// sines once per token (position x frequency reduced to a turn in float64,
-// then a float32 sincos), then D / 16 lanes per head, each with one 16-byte
-// chunk of either half of the head, so that both elements of every pair are
-// in one lane in either layout of the pairs.  A lane keeps its pairs' turns
-// and its weights for all of its heads; its next head is loaded before the
-// last one's is worked on, the first before the angles.
-constexpr int kRopeThreads = 256;
+// A warp takes a token, or a part of its heads: the angles' cosines and sines
+// once (position x frequency reduced to a turn in float64, then a float32
+// sine and cosine), then D / 16 lanes per head, each with one 16-byte chunk of either
+// half of the head, so that both elements of every pair are in one lane in
+// either layout of the pairs.  A lane keeps its pairs' turns and its weights
+// for all of its heads; its next heads, kRopeAhead of them, are on their way
+// to shared memory meanwhile, the first before the angles.  Bound by HBM for
+// prompts.
+constexpr int kRopeThreads = 128, kRopeWarps = kRopeThreads / 32, kRopeAhead = 2;
 
-template <typename T, int D, int WPT, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads, 3) norm_rope_kernel(const NormRopeArgs a) {
-  constexpr int L = D / 16, HW = 32 / L, TOK = kRopeThreads / 32 / WPT;  // lanes per head, heads per warp, tokens
-  __shared__ float2 cs[TOK][D / 2];                        // a lane's i-th turn at [i L + lane]
+template <typename T, int D, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads, 5) norm_rope_kernel(const NormRopeArgs a, int parts) {
+  constexpr int L = D / 16, HW = 32 / L;                   // lanes per head, heads per warp
+  __shared__ float2 cs[kRopeWarps][D / 2];                 // a lane's i-th turn at [i L + lane]
+  __shared__ uint4 buf[kRopeAhead * kRopeThreads * 2];     // [stage][warp][half][lane]
   const int tid = threadIdx.x, lane = tid % L, warp = tid / 32;
-  const int tok0 = (int)blockIdx.x * TOK, tokens = a.batch * a.n, tok = tok0 + warp / WPT;
-  const int step = HW * WPT * (int)gridDim.y;
+  const int64_t part = (int64_t)blockIdx.x * kRopeWarps + warp;
+  const int tok = (int)(part / parts);
+  if (tok >= a.batch * a.n) return;                        // whole warps; they share nothing
+  const int step = HW * parts;
   const int b = tok / a.n, t = tok % a.n;
-  // The lane's next head: of the queries first, then of the keys.
-  bool keys = false;
-  int h = ((int)blockIdx.y * WPT + warp % WPT) * HW + tid % 32 / L, heads = a.Hq;
-  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + b * a.q_row + t * a.q_token + h * a.q_head) + lane;
-  auto settle = [&]() {                                    // from behind the queries to the keys
-    if (!keys && h >= a.Hq) {
-      keys = true, h -= a.Hq, heads = a.Hkv;
-      src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.k) + b * a.k_row + t * a.k_token + h * a.k_head) + lane;
+  // A lane's heads: of the queries first, then of the keys.
+  struct Head {
+    int h, heads;
+    bool keys;
+    __device__ void settle(const NormRopeArgs& a) {        // from behind the queries to the keys
+      if (!keys && h >= a.Hq) keys = true, h -= a.Hq, heads = a.Hkv;
     }
   };
-  if (tok >= tokens) h = a.Hq + a.Hkv;
-  settle();
-  uint4 next[2], wt[2];
-  if (h < heads) next[0] = src[0], next[1] = src[L];
-  for (int i = tid; i < TOK * (D / 2); i += kRopeThreads) {
-    const int u = i / (D / 2), p = i % (D / 2);
-    if (tok0 + u < tokens) {
-      const double turns = 0.15915494309189533577;         // 1 / (2 pi)
-      const double ang = (double)a.positions[tok0 + u] * (double)a.inv_freq[p];
-      const float r = (float)fma(-6.283185307179586476925286766559, rint(ang * turns), ang);
-      float s, c;
-      sincosf(r, &s, &c);
-      cs[u][INTER ? (p % 4 + p / (D / 4) * 4) * L + p % (D / 4) / 4 : p % 8 * L + p / 8] = make_float2(c, s);
+  Head use{(int)(part % parts) * HW + tid % 32 / L, a.Hq, false};
+  use.settle(a);
+  Head get = use;
+  const uint32_t mine = (uint32_t)__cvta_generic_to_shared(buf) + (warp * 64 + tid % 32) * 16;
+  auto fetch = [&](int stage) {
+    if (get.h < get.heads) {
+      const T* src = (get.keys ? static_cast<const T*>(a.k) + b * a.k_row + t * a.k_token + get.h * a.k_head
+                               : static_cast<const T*>(a.q) + b * a.q_row + t * a.q_token + get.h * a.q_head) + 8 * lane;
+      const uint32_t dst = mine + stage * (kRopeThreads * 32);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 512), "l"(src + 8 * L) : "memory");
+      get.h += step;
+      get.settle(a);
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kRopeAhead; ++i) fetch(i);
+  uint4 wt[2];
+  const T* weight = nullptr;                               // whose values wt holds
+  auto weigh = [&](bool keys) {
+    const T* own = static_cast<const T*>(keys ? a.k_weight : a.q_weight);
+    if (own != weight && own) wt[0] = reinterpret_cast<const uint4*>(own)[lane], wt[1] = reinterpret_cast<const uint4*>(own)[lane + L];
+    weight = own;
+  };
+  weigh(use.keys);
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    const int p = tid % 32 + 32 * i;
+    const double inv_pi = 0.31830988618379067154;
+    const double ang = (double)a.positions[tok] * (double)a.inv_freq[p];
+    const float r = (float)fma(ang, inv_pi, -2.0 * rint(ang * inv_pi * 0.5));   // half turns, in [-1, 1]
+    float s, c;
+    sincospif(r, &s, &c);
+    cs[warp][INTER ? (p % 4 + p / (D / 4) * 4) * L + p % (D / 4) / 4 : p % 8 * L + p / 8] = make_float2(c, s);
   }
-  __syncthreads();
+  __syncwarp();
   float2 turn[8];                                          // of the lane's pairs: elements i, i + 8, or 2 i, 2 i + 1
 #pragma unroll
-  for (int i = 0; i < 8; ++i) turn[i] = cs[warp / WPT][i * L + lane];
-  const T* weight = nullptr;                               // whose values wt holds
-  while (h < heads) {                                      // whole groups of L lanes leave together
-    const uint4 cur[2] = {next[0], next[1]};
-    uint4* dst = reinterpret_cast<uint4*>(keys ? static_cast<T*>(a.k_out) + (((size_t)b * a.Hkv + h) * a.n + t) * D
-                                               : static_cast<T*>(a.q_out) + ((size_t)tok * a.Hq + h) * D) + lane;
-    const T* own = static_cast<const T*>(keys ? a.k_weight : a.q_weight);
-    h += step, src += step * (keys ? a.k_head : a.q_head) / 8;
-    settle();
-    if (h < heads) next[0] = src[0], next[1] = src[L];
-    if (own != weight) {
-      weight = own;
-      if (own) wt[0] = reinterpret_cast<const uint4*>(own)[lane], wt[1] = reinterpret_cast<const uint4*>(own)[lane + L];
-    }
+  for (int i = 0; i < 8; ++i) turn[i] = cs[warp][i * L + lane];
+  int stage = 0;
+  while (use.h < use.heads) {                              // whole groups of L lanes leave together
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRopeAhead - 1) : "memory");
+    const uint4* own_buf = buf + stage * (kRopeThreads * 2) + warp * 64 + tid % 32;   // a lane reads what it copied
+    const uint4 cur[2] = {own_buf[0], own_buf[32]};
+    uint4* dst = reinterpret_cast<uint4*>(use.keys ? static_cast<T*>(a.k_out) + (((size_t)b * a.Hkv + use.h) * a.n + t) * D
+                                                   : static_cast<T*>(a.q_out) + ((size_t)tok * a.Hq + use.h) * D) + lane;
+    weigh(use.keys);
+    fetch(stage);
+    stage = stage + 1 == kRopeAhead ? 0 : stage + 1;
+    use.h += step;
+    use.settle(a);
     float x[16];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -329,14 +351,17 @@ cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s) {
 
 template <typename T, int D>
 static cudaError_t launch_rope(const NormRopeArgs& a, cudaStream_t s) {
-  const int tokens = a.batch * a.n, heads = a.Hq + a.Hkv, at_once = 8 * (32 / (D / 16));
-  // Few tokens: eight warps each, their heads over several CTAs.  Many: two warps each, which keep a token's
-  // turns and the weights for all of its heads.
-  const bool many = tokens >= 4096;
-  const dim3 grid(many ? (tokens + 3) / 4 : tokens, many ? 1 : (heads + at_once - 1) / at_once);
-  auto go = [&](auto fn) { fn<<<grid, kRopeThreads, 0, s>>>(a); };
-  if (a.interleaved) many ? go(norm_rope_kernel<T, D, 2, true>) : go(norm_rope_kernel<T, D, 8, true>);
-  else many ? go(norm_rope_kernel<T, D, 2, false>) : go(norm_rope_kernel<T, D, 8, false>);
+  const int64_t tokens = (int64_t)a.batch * a.n;
+  const int passes = (a.Hq + a.Hkv + 32 / (D / 16) - 1) / (32 / (D / 16));
+  // A token's heads are split while there are fewer warps than the card holds (148 SMs x 24): a step's 8 tokens
+  // take 2.6 us so; whole tokens to a warp save the angles of the parts, 47 us against 50 for 12297 tokens in
+  // two parts.
+  const int64_t want = 148 * 24 / tokens;
+  const int parts = (int)(want < 1 ? 1 : want < passes ? want : passes);
+  const unsigned grid = (unsigned)((tokens * parts + kRopeWarps - 1) / kRopeWarps);
+  auto go = [&](auto fn) { fn<<<grid, kRopeThreads, 0, s>>>(a, parts); };
+  if (a.interleaved) go(norm_rope_kernel<T, D, true>);
+  else go(norm_rope_kernel<T, D, false>);
   return cudaGetLastError();
 }
 
