@@ -73,16 +73,6 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
@@ -90,12 +80,6 @@ template <typename T>
 __device__ __forceinline__ bool quad_bad(const uint4& v) {
   return pair_bad<T>(v.x) || pair_bad<T>(v.y) || pair_bad<T>(v.z) || pair_bad<T>(v.w);
 }
-__device__ __forceinline__ float lds32f(uint32_t a) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
-  return v;
-}
-
 // ---- the plan: which tiles a CTA takes -------------------------------------
 __device__ __forceinline__ bool row_valid(const Q8AttendArgs& a, int len, int nr) {
   return len >= 0 && len <= a.c.capacity && nr >= 0 && nr <= a.n;
@@ -215,12 +199,15 @@ struct Shape {
   static constexpr int OROW = D + 4;                       // a row of partial results: o, ml, mv, l
   static constexpr int JOIN = kWarps * ROWS * OROW * 4;
   static constexpr int WALK = kWarps * 2 * (int)sizeof(Walk);
+  static constexpr bool QS = NT > 1;                       // queries in shared memory, not in registers
+  static constexpr int Q = QS ? NT * (D / 16) * 256 + ROWS * 4 : 0;
 };
 // CTAs per SM: what registers and shared memory allow.
 constexpr int ctas_per_sm(int d, int nt) { return nt > 1 ? 2 : d == 128 ? 3 : 4; }
 template <int D, int NT>
 int smem_bytes(int batch) {
-  return Shape<D, NT>::RING + Shape<D, NT>::JOIN + Shape<D, NT>::WALK + 16 + 4 * (2 * batch + 1);
+  using S = Shape<D, NT>;
+  return S::RING + S::JOIN + S::WALK + S::Q + 16 + 4 * (2 * batch + 1);
 }
 
 // Byte of 16-byte chunk c of token r in a slab: the chunks are permuted inside
@@ -242,13 +229,16 @@ __device__ __forceinline__ int slab_at(int r, int c) {
 // index may be permuted as long as both operands are.
 template <typename T, int FMT, int D, int NT>
 struct Pass {
+  using S = Shape<D, NT>;
   static constexpr int KS = D / 16;          // k-steps of the first product, m-tiles of the second
   float o[KS][NT][4];                        // dims 2 mt, 2 mt + 1 of the lane's D / 8, queries 2 tig, 2 tig + 1
   float ml[NT][2], mv[NT][2], l[NT][2];
   float cq[NT][2];                           // sigma log2(e) of the query (and its power of two)
-  int end[NT][2];                            // positions that it sees
-  int min_end;
-  uint32_t qf[NT][KS][2];
+  uint32_t qf[S::QS ? 1 : NT][KS][2];        // the queries' operand, or its place in shared memory
+  uint2* qs;
+  float* qup;
+  int base, r0;                              // query row r of the pass sees positions below base + (r0 + r) / G
+  uint32_t inv_g;                            // 2^16 / G, rounded up: (r inv_g) >> 16 is r / G for r < 2^11
   int lane, gid, tig, warp;
 
   // Query row r of a unit (r = token G + head); rows behind the last one repeat it and are not stored.
@@ -258,114 +248,130 @@ struct Pass {
            (int64_t)(kvh * a.G + r % a.G) * a.head_stride;
   }
 
-  // Loads the queries as the B operand, column 8 t + gid, in fp16: a bf16
-  // query is scaled by the power of two that brings its largest element into
-  // [1, 2), which cq takes back.
-  __device__ __forceinline__ void start(const Q8AttendArgs& a, int row, int kvh, int r0, int len) {
+  // Column 8 t + gid of the queries' operand, as it is.
+  __device__ __forceinline__ void load_q(const Q8AttendArgs& a, int row, int kvh, int t, uint32_t (&f)[KS][2]) {
+    const T* q = q_row(a, row, kvh, r0 + 8 * t + gid) + 16 * tig;
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint4 v = *reinterpret_cast<const uint4*>(q + 64 * j + 8 * x);
+        f[4 * j + 2 * x][0] = v.x, f[4 * j + 2 * x][1] = v.y;
+        f[4 * j + 2 * x + 1][0] = v.z, f[4 * j + 2 * x + 1][1] = v.w;
+      }
+  }
+  // ... in fp16: a bf16 query is scaled by the power of two that brings its
+  // largest element into [1, 2); returns sigma log2(e) by that power.
+  __device__ __forceinline__ float half_q(const Q8AttendArgs& a, uint32_t (&f)[KS][2]) {
+    if (!Pair16<T>::kWide) return a.scale_log2;
+    uint32_t mx = 0;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) mx = __vmaxu2(mx, __vmaxu2(f[s][0] & 0x7fff7fffu, f[s][1] & 0x7fff7fffu));
+    mx = max(mx & 0xffffu, mx >> 16);
+    mx = max(mx, __shfl_xor_sync(~0u, mx, 1));
+    mx = max(mx, __shfl_xor_sync(~0u, mx, 2));
+    const int e = mx >= 0x7f80u ? 0 : min(max((int)(mx >> 7) - 127, -126), 126);   // NaN and infinities pass as they are
+    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float2 w = unpack16<T>(f[s][x]);
+        f[s][x] = pack16<__half>(w.x * down, w.y * down);
+      }
+    return a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+  }
+
+  // The first half of a pass's start: the loads of its queries, before any fetch that they would wait behind.
+  __device__ __forceinline__ void load(const Q8AttendArgs& a, int row, int kvh, int first_row) {
+    r0 = first_row;
+    if (!S::QS) load_q(a, row, kvh, 0, qf[0]);
+  }
+  __device__ __forceinline__ void start(const Q8AttendArgs& a, int row, int kvh, int len) {
 #pragma unroll
     for (int m = 0; m < KS; ++m)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[m][t][e] = 0.f;
-    const int base = len - (a.n_rows ? a.n_rows[row] : a.n) + 1;
-    min_end = base + r0 / a.G;
+    base = len - (a.n_rows ? a.n_rows[row] : a.n) + 1;
+    if (S::QS) {
+      // each warp brings some columns, for all
+#pragma unroll 1
+      for (int t = warp; t < NT; t += kWarps) {
+        uint32_t f[KS][2];
+        load_q(a, row, kvh, t, f);
+        const float up = half_q(a, f);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const T* q = q_row(a, row, kvh, r0 + 8 * t + gid) + 16 * tig;
-#pragma unroll
-      for (int j = 0; j < D / 64; ++j)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint4 v = *reinterpret_cast<const uint4*>(q + 64 * j + 8 * x);
-          qf[t][4 * j + 2 * x][0] = v.x, qf[t][4 * j + 2 * x][1] = v.y;
-          qf[t][4 * j + 2 * x + 1][0] = v.z, qf[t][4 * j + 2 * x + 1][1] = v.w;
-        }
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float up = a.scale_log2;
-      if (Pair16<T>::kWide) {
-        uint32_t mx = 0;
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-          mx = __vmaxu2(mx, __vmaxu2(qf[t][s][0] & 0x7fff7fffu, qf[t][s][1] & 0x7fff7fffu));
-        mx = max(mx & 0xffffu, mx >> 16);
-        mx = max(mx, __shfl_xor_sync(~0u, mx, 1));
-        mx = max(mx, __shfl_xor_sync(~0u, mx, 2));
-        const int e = mx >= 0x7f80u ? 0 : min(max((int)(mx >> 7) - 127, -126), 126);   // NaN and infinities pass as they are
-        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-        up *= __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float2 w = unpack16<T>(qf[t][s][x]);
-            qf[t][s][x] = pack16<__half>(w.x * down, w.y * down);
-          }
+        for (int s = 0; s < KS; ++s) qs[(t * KS + s) * 32 + lane] = make_uint2(f[s][0], f[s][1]);
+        if (tig == 0) qup[8 * t + gid] = up;
       }
+      __syncthreads();
+    }
+    const float up = S::QS ? 0.f : half_q(a, qf[0]);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         ml[t][j] = mv[t][j] = kLowest;
         l[t][j] = 0.f;
-        cq[t][j] = __shfl_sync(~0u, up, 4 * (2 * tig + j));
-        end[t][j] = base + (r0 + 8 * t + 2 * tig + j) / a.G;
+        cq[t][j] = !Pair16<T>::kWide ? a.scale_log2 : S::QS ? qup[8 * t + 2 * tig + j] : __shfl_sync(~0u, up, 4 * (2 * tig + j));
       }
-    }
+  }
+  __device__ __forceinline__ uint2 q_at(int t, int s) {
+    return S::QS ? qs[(t * KS + s) * 32 + lane] : make_uint2(qf[0][s][0], qf[0][s][1]);
+  }
+  __device__ __forceinline__ int end_of(int t, int j) {
+    return base + (int)((uint32_t)(r0 + 8 * t + 2 * tig + j) * inv_g >> 16);
   }
 
-  // Weights of 16 tokens from their logits: denominators are added up here,
-  // the numerators' are returned in `w`.  MASK: a token at position first +
-  // gid (+ 8) counts only before a query's end.
-  __device__ __forceinline__ void weights(const float (&s)[NT][4], const float (&f)[NT][2], float lsv, int first,
-                                          bool mask, float (&w)[NT][4]) {
-    float pl[NT][4];
-    float top_l = kLowest, top_v = kLowest;
-    auto spread = [&]() {
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          pl[t][e] = fmaf(s[t][e], f[t][e & 1], -ml[t][e & 1]);
-          w[t][e] = fmaf(s[t][e], f[t][e & 1], lsv - mv[t][e & 1]);
-        }
-      if (mask)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (first + gid + 8 * (e >> 1) >= end[t][e & 1]) pl[t][e] = w[t][e] = -INFINITY;
-    };
-    spread();
+  // Weights of 16 tokens from their logits x = s f: denominators are added up
+  // here, the numerators' are returned in x.  `mask`: a token at position
+  // first + gid (+ 8) counts only before a query's end.
+  __device__ __forceinline__ void weights(float (&x)[NT][4], const float (&f)[NT][2], float lsv, int first, bool mask) {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) top_l = fmaxf(top_l, pl[t][e]), top_v = fmaxf(top_v, w[t][e]);
-    if (__any_sync(~0u, top_l > kLazy || top_v > kLazy + kShift)) {
+      for (int e = 0; e < 4; ++e) x[t][e] *= f[t][e & 1];
+    if (mask) {
+      const bool nan = isnan(lsv);                         // of the block: for the queries that see it
+      if (nan) lsv = 0.f;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x[t][e] = first + gid + 8 * (e >> 1) >= end_of(t, e & 1) ? -INFINITY : nan ? NAN : x[t][e];
+    }
+    float over = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float m = fmaxf(x[t][j], x[t][j + 2]);
+        over = fmaxf(over, fmaxf(m - ml[t][j], m + (lsv - mv[t][j]) - kShift));
+      }
+    if (__any_sync(~0u, over > kLazy)) {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          // -inf: masked
-          float mx = fmaxf(pl[t][j] == -INFINITY ? kLowest : s[t][j] * f[t][j],
-                           pl[t][j + 2] == -INFINITY ? kLowest : s[t][j + 2] * f[t][j]);
+          float m = fmaxf(x[t][j], x[t][j + 2]);
 #pragma unroll
-          for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
-          const float nl = fmaxf(ml[t][j], mx), nv = mx > kLowest ? fmaxf(mv[t][j], mx + lsv - kShift) : mv[t][j];
+          for (int d = 4; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+          const float nl = fmaxf(ml[t][j], m), nv = fmaxf(mv[t][j], m + lsv - kShift);
           l[t][j] *= ex2(ml[t][j] - nl);
           const float c = ex2(mv[t][j] - nv);
           ml[t][j] = nl, mv[t][j] = nv;
 #pragma unroll
-          for (int m = 0; m < KS; ++m) o[m][t][j] *= c, o[m][t][j + 2] *= c;
+          for (int k = 0; k < KS; ++k) o[k][t][j] *= c, o[k][t][j + 2] *= c;
         }
-      spread();
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        l[t][e & 1] += ex2(pl[t][e]);
-        w[t][e] = ex2(w[t][e]);
+        l[t][e & 1] += ex2(x[t][e] - ml[t][e & 1]);
+        x[t][e] = ex2(x[t][e] + (lsv - mv[t][e & 1]));
       }
   }
 
@@ -373,39 +379,52 @@ struct Pass {
   // `st` with the scales behind it, or of the open block, from the 16-bit
   // ring in global memory.  The open block's products take the cache's own
   // type, exactly; bf16 weights go in as two bf16 parts.
-  __device__ __forceinline__ void tile(const Q8AttendArgs& a, uint32_t st, int tile, bool open, int row, int kvh,
-                                       int r0, int len) {
-    constexpr int SLAB = Shape<D, NT>::SLAB;
+  __device__ __forceinline__ void tile(const Q8AttendArgs& a, const uint8_t* st, int tile, bool open, int row, int kvh,
+                                       int len) {
+    constexpr int SLAB = S::SLAB;
     const int first = tile * kQ8Block + 16 * warp, cnt = len - first;
     if (cnt <= 0) return;                                  // behind the open block's tokens
-    const size_t ring = (((size_t)row * a.c.num_kv_heads + kvh) * kQ8Ring + first % kQ8Ring) * D;
-    float s[NT][4], f[NT][2], w[NT][4], lsv = 0.f;
+    float s[NT][4], f[NT][2], lsv = 0.f;
     uint32_t bad = 0;                                      // the open block's tokens with a NaN or an infinity
+    uint4 vo[4][KS / 4];                                   // its values
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
     if (!open) {
-      const float sk = lds32f(st + 2 * SLAB);
-      lsv = lg2(lds32f(st + 2 * SLAB + 4));
+      const float sk = *reinterpret_cast<const float*>(st + 2 * SLAB);
+      lsv = lg2(*reinterpret_cast<const float*>(st + 2 * SLAB + 4));
 #pragma unroll
       for (int t = 0; t < NT; ++t) f[t][0] = sk * cq[t][0], f[t][1] = sk * cq[t][1];
 #pragma unroll
       for (int j = 0; j < D / 64; ++j) {
-        const uint4 ka = lds128(st + slab_at<D>(gid, tig + 4 * j)), kb = lds128(st + slab_at<D>(gid + 8, tig + 4 * j));
-        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+        const uint4 ka = *reinterpret_cast<const uint4*>(st + slab_at<D>(gid, tig + 4 * j));
+        const uint4 kb = *reinterpret_cast<const uint4*>(st + slab_at<D>(gid + 8, tig + 4 * j));
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           uint32_t a0, a1, a2, a3;
-          codes_to_half4<FMT>(wa[x], a0, a2);
-          codes_to_half4<FMT>(wb[x], a1, a3);
+          codes_to_half4<FMT>(word(ka, x), a0, a2);
+          codes_to_half4<FMT>(word(kb, x), a1, a3);
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
-            mma16816(s[t], a0, a1, a2, a3, qf[t][4 * j + x][0], qf[t][4 * j + x][1], __half());
+          for (int t = 0; t < NT; ++t) {
+            const uint2 b = q_at(t, 4 * j + x);
+            mma16816(s[t], a0, a1, a2, a3, b.x, b.y, __half());
+          }
         }
       }
     } else {
+      const size_t ring = (((size_t)row * a.c.num_kv_heads + kvh) * kQ8Ring + first % kQ8Ring) * D;
+      const T* vr = static_cast<const T*>(a.c.v_recent) + ring + D / 8 * gid;
       const T* kr = static_cast<const T*>(a.c.k_recent) + ring + 16 * tig;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 2 * tig + (i & 1) + 8 * (i >> 1);
+#pragma unroll
+        for (int x = 0; x < KS / 4; ++x) {
+          vo[i][x] = r < cnt ? *reinterpret_cast<const uint4*>(vr + r * D + 8 * x) : make_uint4(0, 0, 0, 0);
+          if (quad_bad<T>(vo[i][x])) bad |= 1u << r;
+        }
+      }
 #pragma unroll
       for (int t = 0; t < NT; ++t) f[t][0] = f[t][1] = a.scale_log2;
 #pragma unroll
@@ -421,36 +440,33 @@ struct Pass {
           }
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            uint32_t b[2][2];
-            if (Pair16<T>::kWide) {                        // the raw query: cached by the load of qf
+            uint2 b0 = q_at(t, 4 * j + 2 * x), b1 = q_at(t, 4 * j + 2 * x + 1);
+            if (Pair16<T>::kWide) {                        // the raw query: cached by the first load of it
               const uint4 v = *reinterpret_cast<const uint4*>(q_row(a, row, kvh, r0 + 8 * t + gid) + 64 * j + 16 * tig + 8 * x);
-              b[0][0] = v.x, b[0][1] = v.y, b[1][0] = v.z, b[1][1] = v.w;
-            } else {
-#pragma unroll
-              for (int e = 0; e < 2; ++e) b[e][0] = qf[t][4 * j + 2 * x + e][0], b[e][1] = qf[t][4 * j + 2 * x + e][1];
+              b0 = make_uint2(v.x, v.y), b1 = make_uint2(v.z, v.w);
             }
-            mma16816(s[t], k[0].x, k[1].x, k[0].y, k[1].y, b[0][0], b[0][1], T());
-            mma16816(s[t], k[0].z, k[1].z, k[0].w, k[1].w, b[1][0], b[1][1], T());
+            mma16816(s[t], k[0].x, k[1].x, k[0].y, k[1].y, b0.x, b0.y, T());
+            mma16816(s[t], k[0].z, k[1].z, k[0].w, k[1].w, b1.x, b1.y, T());
           }
         }
     }
-    weights(s, f, lsv, first, open || (tile + 1) * kQ8Block > min_end, w);
+    weights(s, f, lsv, first, open || (tile + 1) * kQ8Block > base + (int)((uint32_t)r0 * inv_g >> 16));
     if (!open) {
       uint32_t b[NT][2];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        b[t][0] = movmatrix(pack16<__half>(w[t][0], w[t][1]));
-        b[t][1] = movmatrix(pack16<__half>(w[t][2], w[t][3]));
+        b[t][0] = movmatrix(pack16<__half>(s[t][0], s[t][1]));
+        b[t][1] = movmatrix(pack16<__half>(s[t][2], s[t][3]));
       }
       uint32_t v[4][D / 32];                               // tokens 2 tig, 2 tig + 1, + 8, + 9
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = 2 * tig + (i & 1) + 8 * (i >> 1);
         if (D == 128) {
-          const uint4 x = lds128(st + SLAB + slab_at<D>(r, gid));
+          const uint4 x = *reinterpret_cast<const uint4*>(st + SLAB + slab_at<D>(r, gid));
           v[i][0] = x.x, v[i][1] = x.y, v[i][D / 32 - 2] = x.z, v[i][D / 32 - 1] = x.w;
         } else {
-          const uint2 x = lds64(st + SLAB + slab_at<D>(r, gid >> 1) + 8 * (gid & 1));
+          const uint2 x = *reinterpret_cast<const uint2*>(st + SLAB + slab_at<D>(r, gid >> 1) + 8 * (gid & 1));
           v[i][0] = x.x, v[i][1] = x.y;
         }
       }
@@ -467,17 +483,6 @@ struct Pass {
           for (int t = 0; t < NT; ++t) mma16816(o[2 * x + y][t], a0, a1, a2, a3, b[t][0], b[t][1], __half());
         }
     } else {
-      const T* vr = static_cast<const T*>(a.c.v_recent) + ring + D / 8 * gid;
-      uint4 v[4][KS / 4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 2 * tig + (i & 1) + 8 * (i >> 1);
-#pragma unroll
-        for (int x = 0; x < KS / 4; ++x) {
-          v[i][x] = r < cnt ? *reinterpret_cast<const uint4*>(vr + r * D + 8 * x) : make_uint4(0, 0, 0, 0);
-          if (quad_bad<T>(v[i][x])) bad |= 1u << r;
-        }
-      }
       bad = __reduce_or_sync(~0u, bad);
       if (bad) {
         // NaN for the queries that see the token; 0 x NaN would reach the others, so its values go
@@ -485,12 +490,12 @@ struct Pass {
         for (int i = 0; i < 4; ++i)
           if (bad >> (2 * tig + (i & 1) + 8 * (i >> 1)) & 1)
 #pragma unroll
-            for (int x = 0; x < KS / 4; ++x) v[i][x] = make_uint4(0, 0, 0, 0);
+            for (int x = 0; x < KS / 4; ++x) vo[i][x] = make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if ((bad >> (gid + 8 * (e >> 1)) & 1) && first + gid + 8 * (e >> 1) < end[t][e & 1]) w[t][e] = NAN;
+            if ((bad >> (gid + 8 * (e >> 1)) & 1) && first + gid + 8 * (e >> 1) < end_of(t, e & 1)) s[t][e] = NAN;
       }
 #pragma unroll
       for (int part = 0; part < (Pair16<T>::kWide ? 2 : 1); ++part) {
@@ -499,15 +504,15 @@ struct Pass {
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const uint32_t pk = pack16<T>(w[t][2 * e], w[t][2 * e + 1]);
+            const uint32_t pk = pack16<T>(s[t][2 * e], s[t][2 * e + 1]);
             b[t][e] = movmatrix(pk);
             const float2 r = unpack16<T>(pk);
-            w[t][2 * e] -= r.x, w[t][2 * e + 1] -= r.y;
+            s[t][2 * e] -= r.x, s[t][2 * e + 1] -= r.y;
           }
 #pragma unroll
         for (int x = 0; x < KS; ++x) {
-          const uint32_t v0 = word(v[0][x / 4], x % 4), v1 = word(v[1][x / 4], x % 4);
-          const uint32_t v2 = word(v[2][x / 4], x % 4), v3 = word(v[3][x / 4], x % 4);
+          const uint32_t v0 = word(vo[0][x / 4], x % 4), v1 = word(vo[1][x / 4], x % 4);
+          const uint32_t v2 = word(vo[2][x / 4], x % 4), v3 = word(vo[3][x / 4], x % 4);
           const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632);
           const uint32_t a2 = __byte_perm(v2, v3, 0x5410), a3 = __byte_perm(v2, v3, 0x7632);
 #pragma unroll
@@ -546,7 +551,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q8_attend_kernel
   extern __shared__ __align__(128) uint8_t smem[];
   float* area = reinterpret_cast<float*>(smem + S::RING);
   Walk* walks = reinterpret_cast<Walk*>(smem + S::RING + S::JOIN);
-  uint32_t* sums = reinterpret_cast<uint32_t*>(smem + S::RING + S::JOIN + S::WALK);
+  uint8_t* qmem = smem + S::RING + S::JOIN + S::WALK;
+  uint32_t* sums = reinterpret_cast<uint32_t*>(qmem + S::Q);
   const Plan plan{sums + 4, reinterpret_cast<int*>(sums + 4 + a.c.batch + 1)};
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int groups = (a.n * a.G + S::ROWS - 1) / S::ROWS, subs = a.c.num_kv_heads * groups;
@@ -561,7 +567,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q8_attend_kernel
   Pass<T, FMT, D, NT> ps;
   ps.lane = threadIdx.x % 32, ps.warp = threadIdx.x / 32;
   ps.gid = ps.lane / 4, ps.tig = ps.lane % 4;
-  const uint32_t ring = smem_u32(smem) + ps.warp * kStages * S::STAGE;
+  ps.qs = reinterpret_cast<uint2*>(qmem), ps.qup = reinterpret_cast<float*>(qmem + S::Q - S::ROWS * 4);
+  ps.inv_g = (65536u + a.G - 1) / a.G;
   Walk *get = walks + 2 * ps.warp, *use = get + 1;
   *get = walk_first(plan, a.c.batch, subs, t0, t1);
   __syncwarp();
@@ -580,8 +587,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q8_attend_kernel
     const int x = i * 32 + ps.lane;
     dst[i] = slab_at<D>(x / (D / 16), x % (D / 16));
   }
+  const uint32_t ring0 = smem_u32(smem) + ps.warp * kStages * S::STAGE;
   bool fresh = true;                                       // `get` is at a segment that kp, vp have not begun
-  auto fetch = [&](uint32_t st) {
+  auto fetch = [&](int stage) {
     while (more == 0 && get->begin < get->end) {
       if (!fresh) walk_next(get, plan, subs);
       fresh = false;
@@ -606,6 +614,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q8_attend_kernel
       }
     }
     if (more > 0) {
+      const uint32_t st = ring0 + stage * S::STAGE;
 #pragma unroll
       for (int i = 0; i < S::SLAB / 512; ++i) {
         cp_async16(st + dst[i], kp + 512 * i);
@@ -619,39 +628,39 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q8_attend_kernel
   };
 
   // `lag` fetches run ahead before the first tile is used.
-  uint32_t st = ring, ahead = ring;
-  int lag = kStages - 1;
+  int stage = 0, ahead = 0, lag = kStages - 1;
 #pragma unroll 1
   while (use->begin < use->end) {
     const int row = use->row, kvh = use->sub / groups, r0 = use->sub % groups * S::ROWS, len = plan.len[row];
     const int begin = use->begin, end = use->end, whole = use->whole;
     bool started = false;
+    ps.load(a, row, kvh, r0);
 #pragma unroll 1
     for (int tile = begin; tile < end;) {
       const bool open = tile >= whole;
       if (!open || lag > 0) {
         fetch(ahead);
-        ahead = ahead == ring + (kStages - 1) * S::STAGE ? ring : ahead + S::STAGE;
+        ahead = ahead + 1 == kStages ? 0 : ahead + 1;
         if (lag > 0) {
           --lag;
           continue;
         }
       }
-      if (!started) ps.start(a, row, kvh, r0, len), started = true;
+      if (!started) ps.start(a, row, kvh, len), started = true;
       cp_wait<kStages - 1>();
       __syncwarp();
-      ps.tile(a, st, tile, open, row, kvh, r0, len);
+      ps.tile(a, smem + (ps.warp * kStages + stage) * S::STAGE, tile, open, row, kvh, len);
       __syncwarp();                                        // every lane has read before the stage is filled again
-      if (!open) st = st == ring + (kStages - 1) * S::STAGE ? ring : st + S::STAGE;
+      if (!open) stage = stage + 1 == kStages ? 0 : stage + 1;
       ++tile;
     }
     ps.leave(area);
     __syncthreads();
-    // all threads: the four warps' rows together, D / 128 dims of a row each
+    // all threads: the four warps' rows together, four dims of a row each
     const bool all = begin == 0 && end == use->tiles;
     // the run's second result where the unit begins inside it: of two units that a run has parts of, one does
-    const uint32_t unit0 = plan.pre[row] + (uint32_t)use->sub * (kUnitCost + use->tiles) + kUnitCost;
-    float* part = reinterpret_cast<float*>(a.scratch) + ((size_t)blockIdx.x * 2 + (t0 < unit0)) * S::ROWS * S::OROW;
+    const uint32_t place0 = plan.pre[row] + (uint32_t)use->sub * (kUnitCost + use->tiles) + kUnitCost;
+    float* part = reinterpret_cast<float*>(a.scratch) + ((size_t)blockIdx.x * 2 + (t0 < place0)) * S::ROWS * S::OROW;
     const int rows = min(S::ROWS, (a.n_rows ? a.n_rows[row] : a.n) * a.G - r0);
 #pragma unroll 1
     for (int x = threadIdx.x; x < rows * (D / 4); x += kThreads) {
@@ -673,9 +682,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q8_attend_kernel
         t.x += v.x * c, t.y += v.y * c, t.z += v.z * c, t.w += v.w * c;
       }
       if (all) {
-        const int i = (r0 + r) / a.G, h = kvh * a.G + (r0 + r) % a.G;
+        const int i = (int)((uint32_t)(r0 + r) * ps.inv_g >> 16), h = kvh * a.G + (r0 + r) - i * a.G;
         T* out = static_cast<T*>(a.out) + (((size_t)row * a.n + i) * a.Hq + h) * D + d;
-        const float c = sum == 0.f ? 0.f : ex2(gv - gl) / sum;
+        const float c = sum == 0.f ? 0.f : ex2(gv - gl) / sum;   // no token: 0
         *reinterpret_cast<uint2*>(out) = make_uint2(pack16<T>(t.x * c, t.y * c), pack16<T>(t.z * c, t.w * c));
       } else {
         *reinterpret_cast<float4*>(part + r * S::OROW + d) = t;
@@ -783,22 +792,25 @@ __global__ void __launch_bounds__(kThreads) q8_join_kernel(const Q8AttendArgs a,
   out[threadIdx.x] = (T)result(t, gl, gv, sum);
 }
 
-// Query rows of one pass: 8 where a unit has no more, else 16.
-int pick_nt(int rows) { return rows <= 8 ? 1 : 2; }
+// Query rows of one pass, in eights: all of a unit's, up to 32.
+int pick_nt(int rows) { return rows >= 25 ? 4 : (rows + 7) / 8; }
+
+int groups_of(const tq_q8_cache& c, int Hq, int n) {
+  const int rows = n * (Hq / c.num_kv_heads), nt = pick_nt(rows);
+  return (rows + 8 * nt - 1) / (8 * nt);
+}
 
 uint32_t grid_of(const tq_q8_cache& c, int Hq, int n, int num_sms) {
-  const int rows = n * (Hq / c.num_kv_heads), nt = pick_nt(rows);
-  const int64_t tiles = (int64_t)c.batch * c.num_kv_heads * ((rows + 8 * nt - 1) / (8 * nt)) *
-                        (c.capacity / kQ8Block + kUnitCost);
-  const int64_t most = (int64_t)num_sms * ctas_per_sm(c.head_dim, nt), want = (tiles + kMinPlaces - 1) / kMinPlaces;
+  const int64_t places = (int64_t)c.batch * c.num_kv_heads * groups_of(c, Hq, n) * (c.capacity / kQ8Block + kUnitCost);
+  const int64_t most = (int64_t)num_sms * ctas_per_sm(c.head_dim, pick_nt(n * (Hq / c.num_kv_heads)));
+  const int64_t want = (places + kMinPlaces - 1) / kMinPlaces;
   return (uint32_t)(want < most ? want : most);
 }
 
 template <typename T, int FMT, int D, int NT>
 cudaError_t launch(const Q8AttendArgs& a, uint32_t grid, cudaStream_t s) {
-  const int smem = smem_bytes<D, NT>(a.c.batch);
   auto kernel = q8_attend_kernel<T, FMT, D, NT>;
-  // once per device: the most that any batch takes
+  // once per device: the shared memory that the largest batch takes
   static std::atomic<uint64_t> set{0};
   int dev;
   cudaError_t e = cudaGetDevice(&dev);
@@ -809,7 +821,7 @@ cudaError_t launch(const Q8AttendArgs& a, uint32_t grid, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     set.fetch_or(bit, std::memory_order_relaxed);
   }
-  kernel<<<grid, kThreads, smem, s>>>(a);
+  kernel<<<grid, kThreads, smem_bytes<D, NT>(a.c.batch), s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // a programmatic dependent: it waits for the attention kernel before it reads its results
@@ -826,17 +838,25 @@ cudaError_t launch(const Q8AttendArgs& a, uint32_t grid, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, q8_join_kernel<T, D, NT>, a, grid);
 }
 
+template <typename T, int FMT, int D>
+cudaError_t pick(const Q8AttendArgs& a, uint32_t grid, cudaStream_t s) {
+  switch (pick_nt(a.n * a.G)) {
+    case 1: return launch<T, FMT, D, 1>(a, grid, s);
+    case 2: return launch<T, FMT, D, 2>(a, grid, s);
+    case 3: return launch<T, FMT, D, 3>(a, grid, s);
+    default: return launch<T, FMT, D, 4>(a, grid, s);
+  }
+}
+
 template <typename T, int FMT>
 cudaError_t pick(const Q8AttendArgs& a, uint32_t grid, cudaStream_t s) {
-  const bool one = pick_nt(a.n * a.G) == 1;
-  if (a.c.head_dim == 64) return one ? launch<T, FMT, 64, 1>(a, grid, s) : launch<T, FMT, 64, 2>(a, grid, s);
-  return one ? launch<T, FMT, 128, 1>(a, grid, s) : launch<T, FMT, 128, 2>(a, grid, s);
+  return a.c.head_dim == 64 ? pick<T, FMT, 64>(a, grid, s) : pick<T, FMT, 128>(a, grid, s);
 }
 
 }  // namespace
 
 size_t q8_attend_scratch(const tq_q8_cache& c, int Hq, int n, int num_sms) {
-  const int rows = 8 * pick_nt(n * (Hq / c.num_kv_heads));
+  const size_t rows = 8 * (size_t)pick_nt(n * (Hq / c.num_kv_heads));
   return ((size_t)grid_of(c, Hq, n, num_sms) * 2 * rows * (c.head_dim + 4) * 4 + 255) / 256 * 256;
 }
 

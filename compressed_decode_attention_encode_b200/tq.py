@@ -693,7 +693,8 @@ class TQ8Cache:
         if self._elsewhere():
             return self._on_device(self.attention, q, lens, n_rows, out, softmax_scale, scratch)
         raw = torch._C._cuda_getCurrentRawStream(self._index)
-        size = self._scratch_size.get((hq, n))
+        key = hq, n
+        size = self._scratch_size.get(key)
         if size is None:
             size = self.scratch_bytes(hq, n)
         if out is None:

@@ -206,8 +206,8 @@ tq_status tq_evict_window_rows(tq_cache* cache, const void* k_new, const void* v
  * waits for that kernel.  So the kernel that writes q must not signal its
  * dependents early (griddepcontrol.launch_dependents /
  * cudaTriggerProgrammaticLaunchCompletion before its writes of q): ordinary
- * kernels, PyTorch's included, never do, and the library's own kernels do
- * not write q.  Everything else the call reads is read after the wait.
+ * kernels, PyTorch's included, never do, and of the library's own kernels
+ * only tq_qk_norm_rope's writes q, and it does not.  Everything else the call reads is read after the wait.
  */
 tq_status tq_decode_attention(tq_cache* cache, const void* q, float* out,
                               float softmax_scale, cudaStream_t stream);
