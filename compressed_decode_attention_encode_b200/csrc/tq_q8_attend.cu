@@ -10,7 +10,7 @@
 // The work is the batch's tiles (a unit's whole blocks of 64 tokens, then its
 // open block), flattened and cut into equal runs, one per CTA, so that rows of
 // any length share the card; every CTA finds its run from the lengths alone
-// (they are device memory).  Each unit has kUnitCost places before its first
+// (they are device memory).  Each unit has unit_cost places before its first
 // tile, which stand for what a pass costs besides its tiles (its queries'
 // latency, the open block's, the join of the warps).  A unit inside one CTA's
 // run is finished there; the others leave partial results that a second
@@ -25,8 +25,6 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kStages = 2;
-constexpr int kUnitCost = 8;                 // of a unit besides its tiles, in tiles
-constexpr int kMinPlaces = 4;                // that a CTA takes at least
 constexpr float kLowest = -3.0e38f;          // of a reference before its first token
 constexpr float kShift = 7.f;                // numerator weights are 2^7 at their reference (mv holds it less 7),
 constexpr float kLazy = 8.f;                 // and a reference moves when one exceeds it by 2^8: below fp16's 2^16
@@ -84,13 +82,16 @@ __device__ __forceinline__ bool quad_bad(const uint4& v) {
 __device__ __forceinline__ bool row_valid(const Q8AttendArgs& a, int len, int nr) {
   return len >= 0 && len <= a.c.capacity && nr >= 0 && nr <= a.n;
 }
+// What a unit costs besides its tiles, in tiles.  Measured: 33 ragged rows with one query each (NT = 1) take
+// 45 us with 8 and 54 with 4; 5 queries in each of 16 rows (NT = 3, heavier tiles) 33.5 with 8 and 31.6 with 4.
+constexpr int unit_cost(int nt) { return nt == 1 ? 8 : 4; }
 // In shared memory: places before each row [batch + 1], lengths [batch] (0 where a row has no work).
 struct Plan {
   uint32_t* pre;
   int* len;
 };
 // Places before each row (a unit's places x units of a row).
-__device__ __forceinline__ void plan_rows(const Q8AttendArgs& a, int subs, const Plan& p, uint32_t* warp_sums) {
+__device__ __forceinline__ void plan_rows(const Q8AttendArgs& a, int subs, int cost, const Plan& p, uint32_t* warp_sums) {
   uint32_t total = 0;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
 #pragma unroll 1
@@ -101,7 +102,7 @@ __device__ __forceinline__ void plan_rows(const Q8AttendArgs& a, int subs, const
       const int len = a.lens[b], nr = a.n_rows ? a.n_rows[b] : a.n;
       const bool on = row_valid(a, len, nr) && nr > 0 && len > 0;
       p.len[b] = on ? len : 0;
-      v = on ? (uint32_t)(kUnitCost + (len + kQ8Block - 1) / kQ8Block) * subs : 0;
+      v = on ? (uint32_t)(cost + (len + kQ8Block - 1) / kQ8Block) * subs : 0;
     }
     uint32_t s = v;
 #pragma unroll
@@ -123,10 +124,9 @@ __device__ __forceinline__ void plan_rows(const Q8AttendArgs& a, int subs, const
   if (threadIdx.x == 0) p.pre[a.c.batch] = total;
   __syncthreads();
 }
-__device__ __forceinline__ uint32_t plan_ctas(uint32_t places, uint32_t grid) {
-  const uint32_t most = (places + kMinPlaces - 1) / kMinPlaces;
-  return most < grid ? most : grid;
-}
+// A run has one place at least: with few, short rows the tiles' latency is what counts (a row of 1536 tokens with 4
+// kv heads: 7.3 us with one place a CTA, 7.8 with two, 8.8 with four).
+__device__ __forceinline__ uint32_t plan_ctas(uint32_t places, uint32_t grid) { return places < grid ? places : grid; }
 // Runs of places / ctas places, one more in the first ones.
 __device__ __forceinline__ uint32_t cta_start(uint32_t c, uint32_t places, uint32_t ctas) {
   return c * (places / ctas) + min(c, places % ctas);
@@ -147,7 +147,7 @@ struct Walk {
   int whole, tiles, begin, end;            // of the unit: whole blocks, tiles; of the segment: tiles
 };
 // To the next segment; begin == end at the end of the run.  The warp's lanes write the same values.
-__device__ __noinline__ void walk_next(Walk* w, Plan p, int subs) {
+__device__ __noinline__ void walk_next(Walk* w, Plan p, int subs, int cost) {
   Walk x = *w;
   do {
     if (x.left == 0) {
@@ -162,16 +162,16 @@ __device__ __noinline__ void walk_next(Walk* w, Plan p, int subs) {
       x.whole = len / kQ8Block;
       x.tiles = x.whole + (len % kQ8Block != 0);
     }
-    const uint32_t take = min(x.left, (uint32_t)(kUnitCost + x.tiles));
+    const uint32_t take = min(x.left, (uint32_t)(cost + x.tiles));
     x.begin = 0;
-    x.end = (int)take - kUnitCost;
+    x.end = (int)take - cost;
     x.left -= take;
   } while (x.end <= x.begin);
   __syncwarp();
   *w = x;
   __syncwarp();
 }
-__device__ __forceinline__ Walk walk_first(const Plan& p, int batch, int subs, uint32_t t0, uint32_t t1) {
+__device__ __forceinline__ Walk walk_first(const Plan& p, int batch, int subs, int cost, uint32_t t0, uint32_t t1) {
   Walk x;
   int lo = 0, hi = batch;                  // pre[lo] <= t0 < pre[hi]
   while (hi - lo > 1) {
@@ -182,16 +182,17 @@ __device__ __forceinline__ Walk walk_first(const Plan& p, int batch, int subs, u
   const uint32_t off = t0 - p.pre[lo], places = (p.pre[lo + 1] - p.pre[lo]) / subs;
   x.sub = off / places;
   const uint32_t pos = off % places, take = min(t1 - t0, places - pos);
-  x.tiles = (int)places - kUnitCost;
+  x.tiles = (int)places - cost;
   x.whole = p.len[lo] / kQ8Block;
-  x.begin = max((int)pos - kUnitCost, 0);
-  x.end = (int)(pos + take) - kUnitCost;   // <= begin: a run that begins with places alone
+  x.begin = max((int)pos - cost, 0);
+  x.end = (int)(pos + take) - cost;   // <= begin: a run that begins with places alone
   x.left = t1 - t0 - take;
   return x;
 }
 
 template <int D, int NT>
 struct Shape {
+  static constexpr int COST = unit_cost(NT);
   static constexpr int ROWS = 8 * NT;                      // query rows of a unit's pass
   static constexpr int SLAB = 16 * D;                      // bytes of 16 tokens' codes
   static constexpr int STAGE = 2 * SLAB + 16;              // K, V, scales
@@ -200,6 +201,7 @@ struct Shape {
   static constexpr int JOIN = kWarps * ROWS * OROW * 4;
   static constexpr int WALK = kWarps * 2 * (int)sizeof(Walk);
   static constexpr bool QS = NT > 1;                       // queries in shared memory, not in registers
+  static_assert(NT <= kWarps);                             // a warp brings eight of them
   static constexpr int Q = QS ? NT * (D / 16) * 256 + ROWS * 4 : 0;
 };
 // CTAs per SM: what registers and shared memory allow.
@@ -285,7 +287,7 @@ struct Pass {
   // The first half of a pass's start: the loads of its queries, before any fetch that they would wait behind.
   __device__ __forceinline__ void load(const Q8AttendArgs& a, int row, int kvh, int first_row) {
     r0 = first_row;
-    if (!S::QS) load_q(a, row, kvh, 0, qf[0]);
+    if (!S::QS || warp < NT) load_q(a, row, kvh, S::QS ? warp : 0, qf[0]);
   }
   __device__ __forceinline__ void start(const Q8AttendArgs& a, int row, int kvh, int len) {
 #pragma unroll
@@ -296,15 +298,12 @@ struct Pass {
         for (int e = 0; e < 4; ++e) o[m][t][e] = 0.f;
     base = len - (a.n_rows ? a.n_rows[row] : a.n) + 1;
     if (S::QS) {
-      // each warp brings some columns, for all
-#pragma unroll 1
-      for (int t = warp; t < NT; t += kWarps) {
-        uint32_t f[KS][2];
-        load_q(a, row, kvh, t, f);
-        const float up = half_q(a, f);
+      // warp t brings columns 8 t .. 8 t + 7, for all
+      if (warp < NT) {
+        const float up = half_q(a, qf[0]);
 #pragma unroll
-        for (int s = 0; s < KS; ++s) qs[(t * KS + s) * 32 + lane] = make_uint2(f[s][0], f[s][1]);
-        if (tig == 0) qup[8 * t + gid] = up;
+        for (int s = 0; s < KS; ++s) qs[(warp * KS + s) * 32 + lane] = make_uint2(qf[0][s][0], qf[0][s][1]);
+        if (tig == 0) qup[8 * warp + gid] = up;
       }
       __syncthreads();
     }
@@ -556,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q8_attend_kernel
   const Plan plan{sums + 4, reinterpret_cast<int*>(sums + 4 + a.c.batch + 1)};
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int groups = (a.n * a.G + S::ROWS - 1) / S::ROWS, subs = a.c.num_kv_heads * groups;
-  plan_rows(a, subs, plan, sums);
+  plan_rows(a, subs, S::COST, plan, sums);
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < a.c.batch; b += kThreads)
       if (!row_valid(a, a.lens[b], a.n_rows ? a.n_rows[b] : a.n)) atomicOr(a.c.status, kQ8StatusInvalid);
@@ -570,9 +569,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q8_attend_kernel
   ps.qs = reinterpret_cast<uint2*>(qmem), ps.qup = reinterpret_cast<float*>(qmem + S::Q - S::ROWS * 4);
   ps.inv_g = (65536u + a.G - 1) / a.G;
   Walk *get = walks + 2 * ps.warp, *use = get + 1;
-  *get = walk_first(plan, a.c.batch, subs, t0, t1);
+  *get = walk_first(plan, a.c.batch, subs, S::COST, t0, t1);
   __syncwarp();
-  if (get->end <= get->begin) walk_next(get, plan, subs);
+  if (get->end <= get->begin) walk_next(get, plan, subs, S::COST);
   *use = *get;
   __syncwarp();
 
@@ -591,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q8_attend_kernel
   bool fresh = true;                                       // `get` is at a segment that kp, vp have not begun
   auto fetch = [&](int stage) {
     while (more == 0 && get->begin < get->end) {
-      if (!fresh) walk_next(get, plan, subs);
+      if (!fresh) walk_next(get, plan, subs, S::COST);
       fresh = false;
       more = max(min(get->end, get->whole) - get->begin, 0);
       const size_t unit = (size_t)get->row * a.c.num_kv_heads + get->sub / groups;
@@ -659,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q8_attend_kernel
     // all threads: the four warps' rows together, four dims of a row each
     const bool all = begin == 0 && end == use->tiles;
     // the run's second result where the unit begins inside it: of two units that a run has parts of, one does
-    const uint32_t place0 = plan.pre[row] + (uint32_t)use->sub * (kUnitCost + use->tiles) + kUnitCost;
+    const uint32_t place0 = plan.pre[row] + (uint32_t)use->sub * (S::COST + use->tiles) + S::COST;
     float* part = reinterpret_cast<float*>(a.scratch) + ((size_t)blockIdx.x * 2 + (t0 < place0)) * S::ROWS * S::OROW;
     const int rows = min(S::ROWS, (a.n_rows ? a.n_rows[row] : a.n) * a.G - r0);
 #pragma unroll 1
@@ -691,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q8_attend_kernel
         if (d == 0) *reinterpret_cast<float4*>(part + r * S::OROW + D) = make_float4(gl, gv, sum, 0.f);
       }
     }
-    walk_next(use, plan, subs);
+    walk_next(use, plan, subs, S::COST);
     __syncthreads();
   }
 }
@@ -712,7 +711,7 @@ __global__ void __launch_bounds__(kThreads) q8_join_kernel(const Q8AttendArgs a,
   __shared__ float wm[kWarps][3], wo[kWarps][D];
   const int R = a.n * a.G, groups = (R + S::ROWS - 1) / S::ROWS, subs = a.c.num_kv_heads * groups;
   const int row = blockIdx.y, kvh = blockIdx.x / R, r = blockIdx.x % R, i = r / a.G;
-  plan_rows(a, subs, plan, sums);
+  plan_rows(a, subs, S::COST, plan, sums);
   const int len = a.lens[row], nr = a.n_rows ? a.n_rows[row] : a.n;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const bool valid = row_valid(a, len, nr);
@@ -724,8 +723,8 @@ __global__ void __launch_bounds__(kThreads) q8_join_kernel(const Q8AttendArgs a,
     return;
   }
   const uint32_t places = pre[a.c.batch], ctas = plan_ctas(places, grid), unit = (pre[row + 1] - pre[row]) / subs;
-  const uint32_t first = pre[row] + (uint32_t)(kvh * groups + r / S::ROWS) * unit + kUnitCost;
-  const uint32_t c0 = cta_of(first, places, ctas), c1 = cta_of(first + unit - kUnitCost - 1, places, ctas);
+  const uint32_t first = pre[row] + (uint32_t)(kvh * groups + r / S::ROWS) * unit + S::COST;
+  const uint32_t c0 = cta_of(first, places, ctas), c1 = cta_of(first + unit - S::COST - 1, places, ctas);
   if (c0 == c1) return;
   // CTA c's first result, or its second where the unit begins inside its run
   const uint32_t slot0 = cta_start(c0, places, ctas) < first;
@@ -801,10 +800,10 @@ int groups_of(const tq_q8_cache& c, int Hq, int n) {
 }
 
 uint32_t grid_of(const tq_q8_cache& c, int Hq, int n, int num_sms) {
-  const int64_t places = (int64_t)c.batch * c.num_kv_heads * groups_of(c, Hq, n) * (c.capacity / kQ8Block + kUnitCost);
-  const int64_t most = (int64_t)num_sms * ctas_per_sm(c.head_dim, pick_nt(n * (Hq / c.num_kv_heads)));
-  const int64_t want = (places + kMinPlaces - 1) / kMinPlaces;
-  return (uint32_t)(want < most ? want : most);
+  const int nt = pick_nt(n * (Hq / c.num_kv_heads));
+  const int64_t places = (int64_t)c.batch * c.num_kv_heads * groups_of(c, Hq, n) * (c.capacity / kQ8Block + unit_cost(nt));
+  const int64_t most = (int64_t)num_sms * ctas_per_sm(c.head_dim, nt);
+  return (uint32_t)(places < most ? places : most);
 }
 
 template <typename T, int FMT, int D, int NT>
