@@ -322,7 +322,9 @@ __global__ void __launch_bounds__(kRopeThreads, 5) norm_rope_kernel(const NormRo
 }  // namespace
 
 cudaError_t launch_q8_append(const Q8AppendArgs& a, cudaStream_t s) {
-  const dim3 grid((unsigned)((a.n + kQ8Block - 2) / kQ8Block + 1), (unsigned)(a.c.batch * a.c.num_kv_heads), 2);
+  // blocks that n tokens can touch, wherever they begin
+  const int64_t most = ((int64_t)a.n + kQ8Block - 2) / kQ8Block + 1, blocks = a.c.capacity / kQ8Block;
+  const dim3 grid((unsigned)(most < blocks ? most : blocks), (unsigned)(a.c.batch * a.c.num_kv_heads), 2);
   auto go = [&](auto fn) { fn<<<grid, kAppendThreads, 0, s>>>(a); };
   const bool h = a.c.dtype == TQ_DTYPE_FP16, i8 = a.c.format == TQ_Q8_INT8;
 #define TQ_APPEND(D)                                                                            \
@@ -335,7 +337,8 @@ cudaError_t launch_q8_append(const Q8AppendArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s) {
-  const int64_t chunks = (int64_t)a.n * (a.c.head_dim / 8);
+  const int64_t held = a.c.capacity - a.start;               // no row holds more
+  const int64_t chunks = (a.n < held ? a.n : held) * (a.c.head_dim / 8);
   const int per = kReadThreads * kReadItems;
   const dim3 grid((unsigned)((chunks + per - 1) / per), (unsigned)(a.c.batch * a.c.num_kv_heads), 2);
   auto go = [&](auto fn) { fn<<<grid, kReadThreads, 0, s>>>(a); };

@@ -63,7 +63,7 @@ tq_status tq_q8_append(const tq_q8_cache* c, const void* k, const void* v, int64
       !good_stride(k_row_stride) || !good_stride(k_head_stride) || !good_stride(k_token_stride) ||
       !good_stride(v_row_stride) || !good_stride(v_head_stride) || !good_stride(v_token_stride))
     return TQ_ERR_INVALID_ARG;
-  if (n > c->capacity) return TQ_ERR_CAPACITY;
+  if (n > c->capacity && !n_rows) return TQ_ERR_CAPACITY;
   const Q8AppendArgs a{*c, {k, v}, {k_row_stride, v_row_stride}, {k_head_stride, v_head_stride},
                        {k_token_stride, v_token_stride}, n, lens, n_rows};
   return launch_q8_append(a, stream) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;

@@ -584,7 +584,9 @@ class TQ8Cache:
 
     def _elsewhere(self):
         """Whether another device is the current one: the library launches there."""
-        return self._index >= 0 and self._torch._C._cuda_getDevice() != self._index
+        if self._index < 0:
+            raise ValueError("the cache is not on a CUDA device")
+        return self._torch._C._cuda_getDevice() != self._index
 
     def _ints(self, t, what):
         if t.dtype is not self._torch.int32 or t.get_device() != self._index or t.shape != self._shape[:1] \

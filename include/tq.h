@@ -480,7 +480,8 @@ typedef struct tq_q8_cache {
  *   k, v    device 16-bit [B, Hkv, n, d] by strides, in elements, of the
  *           row, the head and the token (d contiguous); strides are
  *           non-negative multiples of 8, addresses multiples of 16 bytes
- *   n       tokens a row at most, >= 0 (0 is a no-op)
+ *   n       tokens a row at most, >= 0 (0 is a no-op); without n_rows more
+ *           than the capacity returns TQ_ERR_CAPACITY
  *   lens    device int32 [B]: tokens that row b holds before the call; the
  *           call leaves it as it is
  *   n_rows  device int32 [B], 0 <= n_rows[b] <= n: row b appends its first
@@ -520,7 +521,8 @@ tq_status tq_q8_attention_bytes(const tq_q8_cache* cache, int32_t num_q_heads, i
  *            of q) among them
  *   n_rows   device int32 [B] or NULL: row b has n_rows[b] <= n queries; what
  *            out holds behind them is left as it was
- *   out      device 16-bit [B, n, Hq, d], contiguous, 16-byte aligned
+ *   out      device 16-bit [B, n, Hq, d], contiguous, 16-byte aligned; it may
+ *            be q itself (with that layout), and must not overlap it otherwise
  *   softmax_scale  sigma; 0 selects 1/sqrt(d)
  *   scratch  device, 256-byte aligned, at least tq_q8_attention_bytes; it
  *            holds nothing between calls, and calls whose GPU work overlaps

@@ -279,6 +279,15 @@ def test_attention_head_groups(hq, h, n):
     run_attention(st, 14, n, hq)
 
 
+@pytest.mark.parametrize("fmt,dtype", [("int8", "bf16"), ("e4m3", "fp16")])
+@pytest.mark.parametrize("hq,n", [(4, 8), (4, 16), (20, 1), (4, 6), (12, 2), (4, 5), (32, 1), (28, 1), (32, 2)])
+def test_attention_pass_widths(hq, n, fmt, dtype):
+    """One to four eights of query rows in a pass, and more than one pass."""
+    st = Stream(3, 2, 128, 448, fmt, dtype)
+    st.append(60, 400, [400, 66, 128])
+    run_attention(st, 61, n, hq)
+
+
 @pytest.mark.parametrize("n,rows", [(1, [0, 1, 1, 0]), (4, [4, 0, 2, 3]), (17, [17, 1, 16, 9]), (64, [64, 33, 0, 5]),
                                     (64, None), (33, None)])
 @pytest.mark.parametrize("d,fmt,dtype", [(128, "e4m3", "bf16"), (64, "int8", "fp16")])
@@ -359,6 +368,30 @@ def test_attention_bad_tokens_reach_only_who_sees_them():
         assert (np.abs(out[0, :, 2:].double().cpu().numpy() - o) <= lim).all()
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_attention_bad_queries_stay_their_own(dtype, bad):
+    """A head whose query is no number gives NaN, its neighbours what they gave."""
+    st = Stream(1, 2, 64, 256, "int8", dtype)
+    st.append(70, 200)
+    q = values(71, (1, 3, 8, 64), dtype, False).cuda()
+    a = st.c.attention(q, st.lens())
+    q[0, 1, 2, 7] = bad
+    b = st.c.attention(q, st.lens())
+    keep = torch.ones(1, 3, 8, dtype=torch.bool)
+    keep[0, 1, 2] = False
+    assert torch.isnan(b[~keep.cuda()]).all() and torch.equal(a[keep.cuda()], b[keep.cuda()])
+
+
+def test_attention_in_place():
+    """out may be q: units in one CTA's run and units that many share."""
+    st = Stream(2, 2, 64, 8192, "e4m3", "bf16")
+    st.append(72, 8000, [8000, 30])
+    q = values(73, (2, 3, 8, 64), "bf16", False).cuda()
+    want = st.c.attention(q, st.lens())
+    assert st.c.attention(q, st.lens(), out=q) is q and torch.equal(q, want)
+
+
 def test_attention_refuses_rows_on_the_device():
     st = Stream(4, 1, 64, 128, "int8", "fp16")
     st.append(32, 100, [100, 10, 20, 30])
@@ -396,6 +429,45 @@ def test_attention_query_strides_streams_and_repeats():
         assert torch.equal(a, b) and torch.equal(a, c)
     with pytest.raises(tq.TQError):
         st.c.attention(q, lens, scratch=scratch[:-256])
+
+
+def test_append_padded_beyond_the_capacity():
+    """A padded batch may be wider than the cache; the rows' own counts decide."""
+    st = Stream(2, 1, 64, 128, "int8", "fp16")
+    st.append(80, 300, [128, 5])
+    st.check()
+    st.c.append(*[torch.zeros(2, 1, 300, 64, dtype=torch.float16, device="cuda")] * 2, st.lens(), torch.tensor([1, 3], **INT))
+    assert st.c.get_status() == 3
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_offsets_beyond_32_bits(fmt):
+    """The last of 40 rows of 2^20 tokens, its codes 5 GB behind the first's,
+    beside a cache of that row alone: the same split, the same bits."""
+    b, cap, d = 40, 2 ** 20, 128
+    big, one = (tq.TQ8Cache(x, 1, d, cap, fmt) for x in (b, 1))
+    g = torch.Generator("cuda").manual_seed(0)
+    for w in "kv":
+        raw = torch.randint(0, 120, (cap, d), generator=g, dtype=torch.uint8, device="cuda")
+        for c in (big, one):
+            getattr(c, w + "_codes")[-1, 0].view(torch.uint8).copy_(raw)
+            getattr(c, w + "_scales")[-1, 0] = torch.linspace(0.5, 2.0, cap // 64, device="cuda") / 50
+            getattr(c, w + "_recent").fill_(0.25)
+    n = cap - 70
+    lens = torch.zeros(b, **INT)
+    lens[-1] = n
+    k, v = values(1, (b, 1, 65, d), "fp16").cuda(), values(2, (b, 1, 65, d), "fp16").cuda()
+    big.append(k, v, lens, torch.tensor([0] * (b - 1) + [65], **INT))
+    one.append(k[-1:], v[-1:], lens[-1:])
+    lens[-1] += 65
+    q = values(3, (b, 2, 4, d), "fp16", False).cuda()
+    out = big.attention(q, lens)
+    assert torch.equal(out[-1:], one.attention(q[-1:], lens[-1:])) and not out[:-1].any() and out[-1].isfinite().all()
+    for x, y in zip(big.read(lens, n - 100, 165), one.read(lens[-1:], n - 100, 165)):
+        assert torch.equal(x[-1:], y) and not x[:-1].any()
+    for x in ("k_codes", "v_codes", "k_scales", "v_scales", "k_recent", "v_recent"):
+        assert torch.equal(getattr(big, x)[-1].view(torch.uint8), getattr(one, x)[-1].view(torch.uint8)), x
+    assert big.get_status() == 0 and one.get_status() == 0
 
 
 # ---- norm and rotation ------------------------------------------------------------
@@ -512,6 +584,31 @@ def test_a_decoding_run_captured_and_replayed():
     y = steps[-1][1]
     q, _ = tq.qk_norm_rope(y[:, :, :hq], y[:, :, hq:hq + h], (lens2 - 1)[:, None].contiguous(), f, w, w)
     check_attention(st, q, out[1])
+
+
+def test_two_graphs_and_an_eager_call_at_once():
+    """Calls on one cache from two graphs and the current stream, replayed side
+    by side: each has its own scratch."""
+    st = Stream(2, 2, 128, 8192, "int8", "fp16")
+    st.append(90, 8100, [8100, 2500])
+    lens = st.lens()
+    qs = [values(91 + i, (2, 1 + 2 * i, 8, 128), "fp16", False).cuda() for i in range(3)]
+    want = [st.c.attention(q, lens).clone() for q in qs]
+    graphs, outs = [], []
+    for q in qs[:2]:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(st.c.attention(q, lens))
+        graphs.append(g)
+    side = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for g, s in zip(graphs, side):
+            with torch.cuda.stream(s):
+                g.replay()
+        got = st.c.attention(qs[2], lens)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want[2]) and torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
 
 
 def test_the_compressed_cache_takes_the_rotated_keys():

@@ -222,3 +222,13 @@ def test_python_calls_refuse_other_tensors(lib):
                                                           for y in ("codes", "scales", "recent")})
     with pytest.raises(ValueError):   # CPU tensors
         tq.qk_norm_rope(q, k.transpose(1, 2), torch.zeros(2, 1, **i), torch.zeros(32))
+
+
+def test_python_calls_need_a_cuda_cache(lib):
+    """A cache of CPU tensors is refused at every call, whatever the box has."""
+    c = tq.TQ8Cache(1, 1, 64, 64, device="cpu")
+    k, lens = torch.zeros(1, 1, 1, 64, dtype=torch.float16), torch.zeros(1, dtype=torch.int32)
+    for call in (lambda: c.append(k, k, lens), lambda: c.read(lens, 0, 1), lambda: c.attention(k, lens),
+                 lambda: c.scratch_bytes(1, 1), lambda: c.get_status()):
+        with pytest.raises(ValueError):
+            call()
