@@ -205,7 +205,7 @@ struct Shape {
   static constexpr int Q = QS ? NT * (D / 16) * 256 + ROWS * 4 : 0;
 };
 // CTAs per SM: what registers and shared memory allow.
-constexpr int ctas_per_sm(int d, int nt) { return nt > 1 ? 2 : d == 128 ? 3 : 4; }
+constexpr int ctas_per_sm(int d, int nt) { return nt == 1 ? (d == 128 ? 3 : 4) : nt == 2 && d == 64 ? 3 : 2; }
 template <int D, int NT>
 int smem_bytes(int batch) {
   using S = Shape<D, NT>;
@@ -791,8 +791,13 @@ __global__ void __launch_bounds__(kThreads) q8_join_kernel(const Q8AttendArgs a,
   out[threadIdx.x] = (T)result(t, gl, gv, sum);
 }
 
-// Query rows of one pass, in eights: all of a unit's, up to 32.
-int pick_nt(int rows) { return rows >= 25 ? 4 : (rows + 7) / 8; }
+// A unit's query rows are cut into passes of up to 24, as even as eights allow.  24 rows are what registers
+// hold: a pass of 32 spilled, and took 81 us (int8, fp16) and 123 us (e4m3, bf16) for 8 queries of 4 heads over 16
+// rows of 4096 tokens (8 kv heads of 128), where two passes of 16 take @@.
+int pick_nt(int rows) {
+  const int eights = (rows + 7) / 8, passes = (eights + 2) / 3;
+  return (eights + passes - 1) / passes;
+}
 
 int groups_of(const tq_q8_cache& c, int Hq, int n) {
   const int rows = n * (Hq / c.num_kv_heads), nt = pick_nt(rows);
@@ -842,8 +847,7 @@ cudaError_t pick(const Q8AttendArgs& a, uint32_t grid, cudaStream_t s) {
   switch (pick_nt(a.n * a.G)) {
     case 1: return launch<T, FMT, D, 1>(a, grid, s);
     case 2: return launch<T, FMT, D, 2>(a, grid, s);
-    case 3: return launch<T, FMT, D, 3>(a, grid, s);
-    default: return launch<T, FMT, D, 4>(a, grid, s);
+    default: return launch<T, FMT, D, 3>(a, grid, s);
   }
 }
 
