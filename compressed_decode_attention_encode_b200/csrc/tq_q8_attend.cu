@@ -90,26 +90,37 @@ struct Plan {
   uint32_t* pre;
   int* len;
 };
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v) {
+  const int lane = threadIdx.x % 32;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const uint32_t y = __shfl_up_sync(~0u, v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
 // Places before each row (a unit's places x units of a row).
 __device__ __forceinline__ void plan_rows(const Q8AttendArgs& a, int subs, int cost, const Plan& p, uint32_t* warp_sums) {
-  uint32_t total = 0;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  auto places = [&](int b) {
+    if (b >= a.c.batch) return 0u;
+    const int len = a.lens[b], nr = a.n_rows ? a.n_rows[b] : a.n;
+    const bool on = row_valid(a, len, nr) && nr > 0 && len > 0;
+    p.len[b] = on ? len : 0;
+    return on ? (uint32_t)(cost + (len + kQ8Block - 1) / kQ8Block) * subs : 0u;
+  };
+  if (a.c.batch <= 32) {                   // every warp for itself: all write the same values
+    const uint32_t v = places(lane), s = warp_scan(v);
+    if (lane < a.c.batch) p.pre[lane] = s - v;
+    if (lane == 31) p.pre[a.c.batch] = s;
+    __syncwarp();
+    return;
+  }
+  uint32_t total = 0;
 #pragma unroll 1
   for (int b0 = 0; b0 < a.c.batch; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
-    uint32_t v = 0;
-    if (b < a.c.batch) {
-      const int len = a.lens[b], nr = a.n_rows ? a.n_rows[b] : a.n;
-      const bool on = row_valid(a, len, nr) && nr > 0 && len > 0;
-      p.len[b] = on ? len : 0;
-      v = on ? (uint32_t)(cost + (len + kQ8Block - 1) / kQ8Block) * subs : 0;
-    }
-    uint32_t s = v;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const uint32_t y = __shfl_up_sync(~0u, s, o);
-      if (lane >= o) s += y;
-    }
+    const uint32_t v = places(b), s = warp_scan(v);
     if (lane == 31) warp_sums[warp] = s;
     __syncthreads();
     uint32_t before = total;
@@ -128,14 +139,20 @@ __device__ __forceinline__ void plan_rows(const Q8AttendArgs& a, int subs, int c
 // kv heads: 7.3 us with one place a CTA, 7.8 with two, 8.8 with four).
 __device__ __forceinline__ uint32_t plan_ctas(uint32_t places, uint32_t grid) { return places < grid ? places : grid; }
 // Runs of places / ctas places, one more in the first ones.
-__device__ __forceinline__ uint32_t cta_start(uint32_t c, uint32_t places, uint32_t ctas) {
-  return c * (places / ctas) + min(c, places % ctas);
-}
-// The CTA whose run holds place t.
-__device__ __forceinline__ uint32_t cta_of(uint32_t t, uint32_t places, uint32_t ctas) {
-  const uint32_t len = places / ctas, more = places % ctas, longer = more * (len + 1);
-  return t < longer ? t / (len + 1) : more + (t - longer) / len;
-}
+struct Runs {
+  uint32_t len, more, ctas;
+  __device__ __forceinline__ Runs(uint32_t places, uint32_t grid) {
+    ctas = plan_ctas(places, grid);
+    len = ctas ? places / ctas : 0;
+    more = places - len * ctas;
+  }
+  __device__ __forceinline__ uint32_t start(uint32_t c) const { return c * len + min(c, more); }
+  // The CTA whose run holds place t.
+  __device__ __forceinline__ uint32_t of(uint32_t t) const {
+    const uint32_t longer = more * (len + 1);
+    return t < longer ? t / (len + 1) : more + (t - longer) / len;
+  }
+};
 
 // A CTA's run, segment by segment: a segment is the run's tiles [begin, end) of one unit (kv head x query
 // group of a row), never empty.  Kept in shared memory, one for what a warp computes and one, ahead of it,
@@ -173,17 +190,18 @@ __device__ __noinline__ void walk_next(Walk* w, Plan p, int subs, int cost) {
 }
 __device__ __forceinline__ Walk walk_first(const Plan& p, int batch, int subs, int cost, uint32_t t0, uint32_t t1) {
   Walk x;
-  int lo = 0, hi = batch;                  // pre[lo] <= t0 < pre[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    (p.pre[mid] <= t0 ? lo : hi) = mid;
-  }
+  // the last row with pre[row] <= t0: of every 32nd, then of 32 (at most 1024 rows)
+  const int lane = threadIdx.x % 32;
+  int lo = 0;
+  if (batch > 32) lo = 32 * (__popc(__ballot_sync(~0u, 32 * lane < batch && p.pre[min(32 * lane, batch)] <= t0)) - 1);
+  lo += __popc(__ballot_sync(~0u, lo + lane < batch && p.pre[min(lo + lane, batch)] <= t0)) - 1;
   x.row = lo;
-  const uint32_t off = t0 - p.pre[lo], places = (p.pre[lo + 1] - p.pre[lo]) / subs;
+  const int len = p.len[lo];
+  x.whole = len / kQ8Block;
+  x.tiles = x.whole + (len % kQ8Block != 0);
+  const uint32_t off = t0 - p.pre[lo], places = cost + x.tiles;
   x.sub = off / places;
-  const uint32_t pos = off % places, take = min(t1 - t0, places - pos);
-  x.tiles = (int)places - cost;
-  x.whole = p.len[lo] / kQ8Block;
+  const uint32_t pos = off - x.sub * places, take = min(t1 - t0, places - pos);
   x.begin = max((int)pos - cost, 0);
   x.end = (int)(pos + take) - cost;   // <= begin: a run that begins with places alone
   x.left = t1 - t0 - take;
@@ -246,8 +264,9 @@ struct Pass {
   // Query row r of a unit (r = token G + head); rows behind the last one repeat it and are not stored.
   __device__ __forceinline__ const T* q_row(const Q8AttendArgs& a, int row, int kvh, int r) {
     r = min(r, a.n * a.G - 1);
-    return static_cast<const T*>(a.q) + row * a.row_stride + r / a.G * a.token_stride +
-           (int64_t)(kvh * a.G + r % a.G) * a.head_stride;
+    const int i = (int)((uint32_t)r * inv_g >> 16);
+    return static_cast<const T*>(a.q) + row * a.row_stride + i * a.token_stride +
+           (int64_t)(kvh * a.G + r - i * a.G) * a.head_stride;
   }
 
   // Column 8 t + gid of the queries' operand, as it is.
@@ -559,9 +578,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q8_attend_kernel
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < a.c.batch; b += kThreads)
       if (!row_valid(a, a.lens[b], a.n_rows ? a.n_rows[b] : a.n)) atomicOr(a.c.status, kQ8StatusInvalid);
-  const uint32_t places = plan.pre[a.c.batch], ctas = plan_ctas(places, gridDim.x);
-  if (blockIdx.x >= ctas) return;
-  const uint32_t t0 = cta_start(blockIdx.x, places, ctas), t1 = cta_start(blockIdx.x + 1, places, ctas);
+  const Runs runs(plan.pre[a.c.batch], gridDim.x);
+  if (blockIdx.x >= runs.ctas) return;
+  const uint32_t t0 = runs.start(blockIdx.x), t1 = runs.start(blockIdx.x + 1);
+  // unit of the row -> kv head (its query group is what is left)
+  auto head_of = [&](int sub) { return groups == 1 ? sub : sub / groups; };
 
   Pass<T, FMT, D, NT> ps;
   ps.lane = threadIdx.x % 32, ps.warp = threadIdx.x / 32;
@@ -590,19 +611,21 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q8_attend_kernel
   bool fresh = true;                                       // `get` is at a segment that kp, vp have not begun
   auto fetch = [&](int stage) {
     while (more == 0 && get->begin < get->end) {
-      if (!fresh) walk_next(get, plan, subs, S::COST);
+      const bool first = fresh;
+      if (!first) walk_next(get, plan, subs, S::COST);
       fresh = false;
       more = max(min(get->end, get->whole) - get->begin, 0);
-      const size_t unit = (size_t)get->row * a.c.num_kv_heads + get->sub / groups;
+      const int kvh = head_of(get->sub);
+      const size_t unit = (size_t)get->row * a.c.num_kv_heads + kvh;
       const size_t at = (unit * a.c.capacity + (size_t)get->begin * kQ8Block + 16 * ps.warp) * D + 16 * ps.lane;
       kp = static_cast<const uint8_t*>(a.c.k_codes) + at;
       vp = static_cast<const uint8_t*>(a.c.v_codes) + at;
       sp = (ps.lane ? a.c.v_scales : a.c.k_scales) + unit * (a.c.capacity / kQ8Block) + get->begin;
       // What the pass reads outside the ring, into L2: behind the fetches in flight it would wait for them all.
-      if (ps.lane < S::ROWS)
+      if (ps.lane < S::ROWS && !first)                     // (the first pass has its queries' loads behind it)
 #pragma unroll
         for (int i = 0; i < D / 64; ++i)
-          prefetch_l2(ps.q_row(a, get->row, get->sub / groups, get->sub % groups * S::ROWS + ps.lane) + 64 * i);
+          prefetch_l2(ps.q_row(a, get->row, kvh, (get->sub - kvh * groups) * S::ROWS + ps.lane) + 64 * i);
       const int cnt = plan.len[get->row] - get->whole * kQ8Block - 16 * ps.warp;
       if (get->end > get->whole && cnt > 0) {
         const size_t open = (unit * kQ8Ring + (get->whole & 1) * kQ8Block + 16 * ps.warp) * D;
@@ -630,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q8_attend_kernel
   int stage = 0, ahead = 0, lag = kStages - 1;
 #pragma unroll 1
   while (use->begin < use->end) {
-    const int row = use->row, kvh = use->sub / groups, r0 = use->sub % groups * S::ROWS, len = plan.len[row];
+    const int row = use->row, kvh = head_of(use->sub), r0 = (use->sub - kvh * groups) * S::ROWS, len = plan.len[row];
     const int begin = use->begin, end = use->end, whole = use->whole;
     bool started = false;
     ps.load(a, row, kvh, r0);
@@ -713,8 +736,15 @@ __global__ void __launch_bounds__(kThreads) q8_join_kernel(const Q8AttendArgs a,
   const int row = blockIdx.y, kvh = blockIdx.x / R, r = blockIdx.x % R, i = r / a.G;
   plan_rows(a, subs, S::COST, plan, sums);
   const int len = a.lens[row], nr = a.n_rows ? a.n_rows[row] : a.n;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const bool valid = row_valid(a, len, nr);
+  const Runs runs(plan.pre[a.c.batch], grid);
+  const uint32_t unit = S::COST + (len + kQ8Block - 1) / kQ8Block;
+  const uint32_t first = plan.pre[row] + (uint32_t)(kvh * groups + r / S::ROWS) * unit + S::COST;
+  uint32_t c0 = 0, c1 = 0;
+  if (valid && len > 0 && nr > 0) c0 = runs.of(first), c1 = runs.of(first + unit - S::COST - 1);
+  // CTA c's first result, or its second where the unit begins inside its run
+  const uint32_t slot0 = runs.start(c0) < first;
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // until here nothing of the attention kernel is read
   if (valid && i >= nr) return;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   T* out = static_cast<T*>(a.out) + (((size_t)row * a.n + i) * a.Hq + kvh * a.G + r % a.G) * D;
@@ -722,12 +752,7 @@ __global__ void __launch_bounds__(kThreads) q8_join_kernel(const Q8AttendArgs a,
     if (threadIdx.x < D) out[threadIdx.x] = valid ? (T)0.f : (T)__uint_as_float(0x7fffffffu);
     return;
   }
-  const uint32_t places = pre[a.c.batch], ctas = plan_ctas(places, grid), unit = (pre[row + 1] - pre[row]) / subs;
-  const uint32_t first = pre[row] + (uint32_t)(kvh * groups + r / S::ROWS) * unit + S::COST;
-  const uint32_t c0 = cta_of(first, places, ctas), c1 = cta_of(first + unit - S::COST - 1, places, ctas);
   if (c0 == c1) return;
-  // CTA c's first result, or its second where the unit begins inside its run
-  const uint32_t slot0 = cta_start(c0, places, ctas) < first;
   const float* part = reinterpret_cast<const float*>(a.scratch) + (size_t)(r % S::ROWS) * S::OROW;
   float gl = kLowest, gv = kLowest, sum = 0.f, o[E];
 #pragma unroll
