@@ -34,6 +34,7 @@ __global__ void __launch_bounds__(kAppendThreads) q8_append_kernel(const Q8Appen
   constexpr int ITEMS = kQ8Block * CH / kAppendThreads;  // chunks per thread
   __shared__ unsigned red[kAppendThreads / 32];
   const int unit = blockIdx.y, kv = blockIdx.z, tid = threadIdx.x;
+  wait_for_stream();
   const int b = unit / a.c.num_kv_heads, h = unit % a.c.num_kv_heads;
   const int len = a.lens[b], fresh = a.n_rows ? a.n_rows[b] : a.n;
   const bool invalid = len < 0 || fresh < 0 || fresh > a.n;
@@ -137,6 +138,7 @@ template <typename T, int FMT, int D>
 __global__ void __launch_bounds__(kReadThreads) q8_read_kernel(const Q8ReadArgs a) {
   constexpr int CH = D / 8;
   const int unit = blockIdx.y, kv = blockIdx.z, b = unit / a.c.num_kv_heads;
+  wait_for_stream();
   const int len = a.lens[b];
   if (len < 0 || len > a.c.capacity) {
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.c.status, kQ8StatusInvalid);
@@ -200,6 +202,7 @@ __global__ void __launch_bounds__(kRopeThreads, 5) norm_rope_kernel(const NormRo
   const int tok = (int)(part / parts);
   if (tok >= a.batch * a.n) return;                        // whole warps; they share nothing
   const int step = HW * parts;
+  wait_for_stream();
   const int b = tok / a.n, t = tok % a.n;
   // A lane's heads: of the queries first, then of the keys.
   struct Head {
@@ -325,7 +328,8 @@ cudaError_t launch_q8_append(const Q8AppendArgs& a, cudaStream_t s) {
   // blocks that n tokens can touch, wherever they begin
   const int64_t most = ((int64_t)a.n + kQ8Block - 2) / kQ8Block + 1, blocks = a.c.capacity / kQ8Block;
   const dim3 grid((unsigned)(most < blocks ? most : blocks), (unsigned)(a.c.batch * a.c.num_kv_heads), 2);
-  auto go = [&](auto fn) { fn<<<grid, kAppendThreads, 0, s>>>(a); };
+  cudaError_t e = cudaSuccess;
+  auto go = [&](auto fn) { e = launch_dependent(fn, grid, kAppendThreads, 0, s, a); };
   const bool h = a.c.dtype == TQ_DTYPE_FP16, i8 = a.c.format == TQ_Q8_INT8;
 #define TQ_APPEND(D)                                                                            \
   h ? (i8 ? go(q8_append_kernel<__half, TQ_Q8_INT8, D>) : go(q8_append_kernel<__half, TQ_Q8_E4M3, D>)) \
@@ -333,7 +337,7 @@ cudaError_t launch_q8_append(const Q8AppendArgs& a, cudaStream_t s) {
   if (a.c.head_dim == 64) TQ_APPEND(64);
   else TQ_APPEND(128);
 #undef TQ_APPEND
-  return cudaGetLastError();
+  return e;
 }
 
 cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s) {
@@ -341,7 +345,8 @@ cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s) {
   const int64_t chunks = (a.n < held ? a.n : held) * (a.c.head_dim / 8);
   const int per = kReadThreads * kReadItems;
   const dim3 grid((unsigned)((chunks + per - 1) / per), (unsigned)(a.c.batch * a.c.num_kv_heads), 2);
-  auto go = [&](auto fn) { fn<<<grid, kReadThreads, 0, s>>>(a); };
+  cudaError_t e = cudaSuccess;
+  auto go = [&](auto fn) { e = launch_dependent(fn, grid, kReadThreads, 0, s, a); };
   const bool h = a.c.dtype == TQ_DTYPE_FP16, i8 = a.c.format == TQ_Q8_INT8;
 #define TQ_READ(D)                                                                              \
   h ? (i8 ? go(q8_read_kernel<__half, TQ_Q8_INT8, D>) : go(q8_read_kernel<__half, TQ_Q8_E4M3, D>)) \
@@ -349,7 +354,7 @@ cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s) {
   if (a.c.head_dim == 64) TQ_READ(64);
   else TQ_READ(128);
 #undef TQ_READ
-  return cudaGetLastError();
+  return e;
 }
 
 template <typename T, int D>
@@ -362,10 +367,11 @@ static cudaError_t launch_rope(const NormRopeArgs& a, cudaStream_t s) {
   const int64_t want = 148 * 24 / tokens;
   const int parts = (int)(want < 1 ? 1 : want < passes ? want : passes);
   const unsigned grid = (unsigned)((tokens * parts + kRopeWarps - 1) / kRopeWarps);
-  auto go = [&](auto fn) { fn<<<grid, kRopeThreads, 0, s>>>(a, parts); };
+  cudaError_t e = cudaSuccess;
+  auto go = [&](auto fn) { e = launch_dependent(fn, dim3(grid), kRopeThreads, 0, s, a, parts); };
   if (a.interleaved) go(norm_rope_kernel<T, D, true>);
   else go(norm_rope_kernel<T, D, false>);
-  return cudaGetLastError();
+  return e;
 }
 
 cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t s) {

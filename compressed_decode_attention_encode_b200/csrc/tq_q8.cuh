@@ -73,6 +73,25 @@ cudaError_t launch_q8_attend(const Q8AttendArgs& a, int num_sms, cudaStream_t s)
 cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t s);
 
 #ifdef __CUDACC__
+// Launches a kernel as a programmatic dependent of the stream's last one: its
+// blocks are placed while that one ends.  The kernel begins with
+// wait_for_stream(), before it reads anything.
+template <typename... P, typename... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---- 16-bit values and codes in registers --------------------------------
 template <typename T>
 struct Pair16;                       // the packed pair of a 16-bit type

@@ -572,7 +572,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q8_attend_kernel
   uint8_t* qmem = smem + S::RING + S::JOIN + S::WALK;
   uint32_t* sums = reinterpret_cast<uint32_t*>(qmem + S::Q);
   const Plan plan{sums + 4, reinterpret_cast<int*>(sums + 4 + a.c.batch + 1)};
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_for_stream();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join's blocks, as this grid leaves room
   const int groups = (a.n * a.G + S::ROWS - 1) / S::ROWS, subs = a.c.num_kv_heads * groups;
   plan_rows(a, subs, S::COST, plan, sums);
   if (blockIdx.x == 0)
@@ -744,7 +745,7 @@ __global__ void __launch_bounds__(kThreads) q8_join_kernel(const Q8AttendArgs a,
   if (valid && len > 0 && nr > 0) c0 = runs.of(first), c1 = runs.of(first + unit - S::COST - 1);
   // CTA c's first result, or its second where the unit begins inside its run
   const uint32_t slot0 = runs.start(c0) < first;
-  asm volatile("griddepcontrol.wait;" ::: "memory");       // until here nothing of the attention kernel is read
+  wait_for_stream();                                       // until here nothing of the attention kernel is read
   if (valid && i >= nr) return;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   T* out = static_cast<T*>(a.out) + (((size_t)row * a.n + i) * a.Hq + kvh * a.G + r % a.G) * D;
@@ -850,21 +851,10 @@ cudaError_t launch(const Q8AttendArgs& a, uint32_t grid, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     set.fetch_or(bit, std::memory_order_relaxed);
   }
-  kernel<<<grid, kThreads, smem_bytes<D, NT>(a.c.batch), s>>>(a);
-  e = cudaGetLastError();
+  e = launch_dependent(kernel, dim3(grid), kThreads, smem_bytes<D, NT>(a.c.batch), s, a);
   if (e != cudaSuccess) return e;
-  // a programmatic dependent: it waits for the attention kernel before it reads its results
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.c.num_kv_heads * a.n * a.G), (unsigned)a.c.batch);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = 4 * (2 * a.c.batch + 1);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, q8_join_kernel<T, D, NT>, a, grid);
+  return launch_dependent(q8_join_kernel<T, D, NT>, dim3((unsigned)(a.c.num_kv_heads * a.n * a.G), (unsigned)a.c.batch),
+                          kThreads, 4 * (2 * a.c.batch + 1), s, a, grid);
 }
 
 template <typename T, int FMT, int D>
