@@ -514,6 +514,9 @@ def _q8_dtypes():
     return {torch.float16: 0, torch.bfloat16: 1}
 
 
+_torch = None        # the module, once a call has needed it
+
+
 def _raw_stream(torch, index: int, stream) -> int:
     """The stream to launch on: ``stream``, or PyTorch's current one of the
     device.  The device must be the current one (the library launches there)."""
@@ -689,26 +692,31 @@ class TQ8Cache:
         if not 3 <= dims <= 4 or shape[0] != b or shape[-1] != d:
             raise ValueError(f"q: expected [{b}, n, Hq, {d}]")
         n, hq = (shape[1], shape[2]) if dims == 4 else (1, shape[1])
-        qp, qs = self._values(q, "q")
+        index = self._index
+        if q.dtype is not self.dtype or q.get_device() != index:
+            raise ValueError(f"q: expected {self.dtype} on {self.device}")
+        qs = q.stride()
+        if qs[-1] != 1:
+            raise ValueError("q: the head dimension must be contiguous")
         lp = self._ints(lens, "lens")
         rp = None if n_rows is None else self._ints(n_rows, "n_rows")
         if self._elsewhere():
             return self._on_device(self.attention, q, lens, n_rows, out, softmax_scale, scratch)
-        raw = torch._C._cuda_getCurrentRawStream(self._index)
+        raw = torch._C._cuda_getCurrentRawStream(index)
         key = hq, n
         size = self._scratch_size.get(key)
         if size is None:
             size = self.scratch_bytes(hq, n)
         if out is None:
             out = torch.empty(shape, dtype=self.dtype, device=self.device)
-        elif out.shape != shape or out.dtype is not self.dtype or out.get_device() != self._index \
+        elif out.shape != shape or out.dtype is not self.dtype or out.get_device() != index \
                 or not out.is_contiguous():
             raise ValueError("out: expected a contiguous tensor of q's shape and type")
         if scratch is None:
             scratch = self._take_scratch(size, raw)
-        elif scratch.dtype is not torch.uint8 or scratch.get_device() != self._index or not scratch.is_contiguous():
+        elif scratch.dtype is not torch.uint8 or scratch.get_device() != index or not scratch.is_contiguous():
             raise ValueError(f"scratch: expected a contiguous uint8 tensor on {self.device}")
-        code = self._lib.tq_q8_attention(self._ref, qp, qs[0], qs[1] if dims == 4 else 0, qs[-2], hq, n, lp, rp,
+        code = self._lib.tq_q8_attention(self._ref, q.data_ptr(), qs[0], qs[1] if dims == 4 else 0, qs[-2], hq, n, lp, rp,
                                          softmax_scale, out.data_ptr(), scratch.data_ptr(), scratch.shape[0], raw)
         if code:
             _check(code, "tq_q8_attention")
@@ -728,43 +736,59 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e
     contiguous, e.g. slices of a packed projection), positions int32 [B, n],
     inv_freq float32 [d / 2].  Returns q_out [B, n, Hq, d] and k_out
     [B, Hkv, n, d], the layouts that the caches' calls take."""
-    import torch
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    torch = _torch
     if stream is not None:                               # what is allocated here belongs to the call's stream
         if stream.device != q.device:
             raise ValueError(f"expected a stream of {q.device}")
         with torch.cuda.stream(stream):
             return qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, q_out, k_out)
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError("expected q [B, n, Hq, d] and k [B, n, Hkv, d]")
-    b, n, hq, d = q.shape
-    b2, n2, hk, d2 = k.shape
-    index, dtype = q.get_device(), q.dtype
+    qs, ks, dtype, index = q.shape, k.shape, q.dtype, q.get_device()
     code = 0 if dtype is torch.float16 else 1 if dtype is torch.bfloat16 else -1
-    if b != b2 or n != n2 or d != d2 or code < 0 or k.dtype is not dtype or index < 0 or k.get_device() != index:
+    if len(qs) != 4 or len(ks) != 4 or qs[:2] != ks[:2] or qs[3] != ks[3] or code < 0 or k.dtype is not dtype \
+            or index < 0 or k.get_device() != index:
         raise ValueError("expected q [B, n, Hq, d] and k [B, n, Hkv, d], CUDA float16 or bfloat16 of one type and device")
-    qs, ks = q.stride(), k.stride()
-    if (qs[3] != 1 and q.numel()) or (ks[3] != 1 and k.numel()):
+    b, n, hq, d = qs
+    hk = ks[2]
+    s0, s1, s2, s3 = q.stride()
+    t0, t1, t2, t3 = k.stride()
+    if (s3 != 1 and q.numel()) or (t3 != 1 and k.numel()):
         raise ValueError("q, k: the head dimension must be contiguous")
     if q_out is None:
         q_out = torch.empty((b, n, hq, d), dtype=dtype, device=q.device)
+    elif q_out.dtype is not dtype or q_out.shape != qs or q_out.get_device() != index or not q_out.is_contiguous():
+        raise ValueError(f"q_out: expected a contiguous {dtype} {list(qs)} on cuda:{index}")
     if k_out is None:
         k_out = torch.empty((b, hk, n, d), dtype=dtype, device=q.device)
-    for t, what, shape, dt in ((positions, "positions", (b, n), torch.int32), (inv_freq, "inv_freq", (d // 2,), torch.float32),
-                               (q_weight, "q_weight", (d,), dtype), (k_weight, "k_weight", (d,), dtype),
-                               (q_out, "q_out", (b, n, hq, d), dtype), (k_out, "k_out", (b, hk, n, d), dtype)):
-        if t is None:
-            if what in ("positions", "inv_freq"):
-                raise ValueError(f"{what} is needed")
-        elif t.shape != shape or t.dtype is not dt or t.get_device() != index or not t.is_contiguous():
-            raise ValueError(f"{what}: expected a contiguous {dt} {list(shape)} on cuda:{index}")
-    if torch._C._cuda_getDevice() != index:
+    elif k_out.dtype is not dtype or k_out.shape != (b, hk, n, d) or k_out.get_device() != index \
+            or not k_out.is_contiguous():
+        raise ValueError(f"k_out: expected a contiguous {dtype} {[b, hk, n, d]} on cuda:{index}")
+    if positions.dtype is not torch.int32 or positions.shape != (b, n) or positions.get_device() != index \
+            or not positions.is_contiguous():
+        raise ValueError(f"positions: expected a contiguous int32 {[b, n]} on cuda:{index}")
+    if inv_freq.dtype is not torch.float32 or inv_freq.shape != (d // 2,) or inv_freq.get_device() != index \
+            or not inv_freq.is_contiguous():
+        raise ValueError(f"inv_freq: expected a contiguous float32 {[d // 2]} on cuda:{index}")
+    if q_weight is not None:
+        if q_weight.dtype is not dtype or q_weight.shape != (d,) or q_weight.get_device() != index \
+                or not q_weight.is_contiguous():
+            raise ValueError(f"q_weight: expected a contiguous {dtype} {[d]} on cuda:{index}")
+        q_weight = q_weight.data_ptr()
+    if k_weight is not None:
+        if k_weight.dtype is not dtype or k_weight.shape != (d,) or k_weight.get_device() != index \
+                or not k_weight.is_contiguous():
+            raise ValueError(f"k_weight: expected a contiguous {dtype} {[d]} on cuda:{index}")
+        k_weight = k_weight.data_ptr()
+    args = (b, n, hq, hk, d, code, q.data_ptr(), s0, s1, s2, k.data_ptr(), t0, t1, t2, positions.data_ptr(),
+            inv_freq.data_ptr(), q_weight, k_weight, eps, 1 if interleaved else 0, q_out.data_ptr(), k_out.data_ptr())
+    if torch._C._cuda_getDevice() == index:
+        code = lib().tq_qk_norm_rope(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
         with torch.cuda.device(index):
-            return qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, q_out, k_out)
-    code = lib().tq_qk_norm_rope(b, n, hq, hk, d, code, q.data_ptr(), qs[0], qs[1], qs[2], k.data_ptr(), ks[0],
-                                 ks[1], ks[2], positions.data_ptr(), inv_freq.data_ptr(),
-                                 None if q_weight is None else q_weight.data_ptr(),
-                                 None if k_weight is None else k_weight.data_ptr(), eps, 1 if interleaved else 0,
-                                 q_out.data_ptr(), k_out.data_ptr(), torch._C._cuda_getCurrentRawStream(index))
+            code = lib().tq_qk_norm_rope(*args, torch._C._cuda_getCurrentRawStream(index))
     if code:
         _check(code, "tq_qk_norm_rope")
     return q_out, k_out
