@@ -94,16 +94,14 @@ __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol
 
 // ---- 16-bit values and codes in registers --------------------------------
 template <typename T>
-struct Pair16;                       // the packed pair of a 16-bit type
+struct Pair16;                           // of a 16-bit type: two infinities, ...
 template <>
 struct Pair16<__half> {
-  using type = __half2;
   static constexpr uint32_t kInf = 0x7c007c00u;
   static constexpr bool kWide = false;   // whether squares of values can leave float32
 };
 template <>
 struct Pair16<__nv_bfloat16> {
-  using type = __nv_bfloat162;
   static constexpr uint32_t kInf = 0x7f807f80u;
   static constexpr bool kWide = true;
 };

@@ -78,6 +78,7 @@ template <typename T>
 __device__ __forceinline__ bool quad_bad(const uint4& v) {
   return pair_bad<T>(v.x) || pair_bad<T>(v.y) || pair_bad<T>(v.z) || pair_bad<T>(v.w);
 }
+
 // ---- the plan: which tiles a CTA takes -------------------------------------
 __device__ __forceinline__ bool row_valid(const Q8AttendArgs& a, int len, int nr) {
   return len >= 0 && len <= a.c.capacity && nr >= 0 && nr <= a.n;

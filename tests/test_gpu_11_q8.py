@@ -315,6 +315,18 @@ def test_attention_ragged_rows():
     run_attention(st, 21, 1, 8)
 
 
+def test_attention_most_rows():
+    """1024 rows, a third of them empty; one query each, and three."""
+    lens = [0 if i % 3 == 1 else (37 * i) % 200 for i in range(1024)]
+    st = Stream(1024, 1, 64, 256, "int8", "fp16")
+    st.append(62, max(lens), lens)
+    for n in (1, 3):
+        q = values(63 + n, (1024, n, 8, 64), "fp16", False).cuda()
+        out = st.c.attention(q, st.lens())
+        check_attention(st, q, out, only=list(range(0, 1024, 37)) + [1021, 1022, 1023])
+        assert not out[1::3].any()
+
+
 @pytest.mark.parametrize("sigma", [1e-4, 0.5, 4.0, -0.3])
 def test_attention_scales(sigma):
     """Flat and one-hot softmaxes: weights over many orders of magnitude."""
