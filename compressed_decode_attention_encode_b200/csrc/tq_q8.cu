@@ -26,10 +26,12 @@ __device__ __forceinline__ float q8_top() {
 // tokens from the ring half of its parity, so a later block of that parity
 // leaves its ring tokens to the first CTA, which writes them after its
 // reads.  So no CTA writes what another one reads.
-constexpr int kAppendThreads = 256;
+// Threads of a CTA: four chunks of 8 values each.
+__host__ __device__ constexpr int append_threads(int d) { return 2 * d; }
 
 template <typename T, int FMT, int D>
-__global__ void __launch_bounds__(kAppendThreads) q8_append_kernel(const Q8AppendArgs a) {
+__global__ void __launch_bounds__(append_threads(D)) q8_append_kernel(const Q8AppendArgs a) {
+  constexpr int kAppendThreads = append_threads(D);
   constexpr int CH = D / 8;                              // 16-byte chunks per token
   constexpr int ITEMS = kQ8Block * CH / kAppendThreads;  // chunks per thread
   __shared__ unsigned red[kAppendThreads / 32];
@@ -329,7 +331,7 @@ cudaError_t launch_q8_append(const Q8AppendArgs& a, cudaStream_t s) {
   const int64_t most = ((int64_t)a.n + kQ8Block - 2) / kQ8Block + 1, blocks = a.c.capacity / kQ8Block;
   const dim3 grid((unsigned)(most < blocks ? most : blocks), (unsigned)(a.c.batch * a.c.num_kv_heads), 2);
   cudaError_t e = cudaSuccess;
-  auto go = [&](auto fn) { e = launch_dependent(fn, grid, kAppendThreads, 0, s, a); };
+  auto go = [&](auto fn) { e = launch_dependent(fn, grid, append_threads(a.c.head_dim), 0, s, a); };
   const bool h = a.c.dtype == TQ_DTYPE_FP16, i8 = a.c.format == TQ_Q8_INT8;
 #define TQ_APPEND(D)                                                                            \
   h ? (i8 ? go(q8_append_kernel<__half, TQ_Q8_INT8, D>) : go(q8_append_kernel<__half, TQ_Q8_E4M3, D>)) \
