@@ -560,10 +560,6 @@ struct Pass {
   }
 };
 
-__device__ __forceinline__ float result(float o, float ml, float mv, float l) {
-  return l == 0.f ? 0.f : o * (ex2(mv - ml) / l);
-}
-
 template <typename T, int FMT, int D, int NT>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q8_attend_kernel(const Q8AttendArgs a) {
   using S = Shape<D, NT>;
@@ -720,13 +716,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q8_attend_kernel
   }
 }
 
-// Joins the partial results of units that several CTAs share, one block per
+// Joins the partial results of units that several CTAs share, WPR warps per
 // (unit, query row), and writes what no CTA had work for: zeros for rows
 // without tokens, NaN for rows whose length is refused.  It is bound by the
-// latency of its loads: the warps take the results in turn, a warp 32 of them
-// at a time, each lane first one result's references and sum, then all lanes
-// D / 32 dims of every result, the loads of eight together.
-template <typename T, int D, int NT>
+// latency of its loads: a row's warps take the results in turn, a warp 32 of
+// them at a time, each lane first one result's references and sum, then all
+// lanes D / 32 dims of every result, the loads of eight together.
+template <typename T, int D, int NT, int WPR>
 __global__ void __launch_bounds__(kThreads) q8_join_kernel(const Q8AttendArgs a, uint32_t grid) {
   using S = Shape<D, NT>;
   constexpr int E = D / 32;
@@ -734,8 +730,10 @@ __global__ void __launch_bounds__(kThreads) q8_join_kernel(const Q8AttendArgs a,
   const Plan plan{pre, reinterpret_cast<int*>(pre + a.c.batch + 1)};
   __shared__ uint32_t sums[kWarps];
   __shared__ float wm[kWarps][3], wo[kWarps][D];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, part_of = warp % WPR;
   const int R = a.n * a.G, groups = (R + S::ROWS - 1) / S::ROWS, subs = a.c.num_kv_heads * groups;
-  const int row = blockIdx.y, kvh = blockIdx.x / R, r = blockIdx.x % R, i = r / a.G;
+  const int ur = (int)blockIdx.x * (kWarps / WPR) + warp / WPR;   // query row among the batch row's units
+  const int row = blockIdx.y, kvh = ur / R, r = ur % R, i = r / a.G;
   plan_rows(a, subs, S::COST, plan, sums);
   const int len = a.lens[row], nr = a.n_rows ? a.n_rows[row] : a.n;
   const bool valid = row_valid(a, len, nr);
@@ -743,15 +741,14 @@ __global__ void __launch_bounds__(kThreads) q8_join_kernel(const Q8AttendArgs a,
   const uint32_t unit = S::COST + (len + kQ8Block - 1) / kQ8Block;
   const uint32_t first = plan.pre[row] + (uint32_t)(kvh * groups + r / S::ROWS) * unit + S::COST;
   uint32_t c0 = 0, c1 = 0;
-  if (valid && len > 0 && nr > 0) c0 = runs.of(first), c1 = runs.of(first + unit - S::COST - 1);
+  if (valid && len > 0 && nr > 0 && kvh < a.c.num_kv_heads) c0 = runs.of(first), c1 = runs.of(first + unit - S::COST - 1);
   // CTA c's first result, or its second where the unit begins inside its run
   const uint32_t slot0 = runs.start(c0) < first;
   wait_for_stream();                                       // until here nothing of the attention kernel is read
-  if (valid && i >= nr) return;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  if (kvh >= a.c.num_kv_heads || (valid && i >= nr)) return;      // all warps of a row alike
   T* out = static_cast<T*>(a.out) + (((size_t)row * a.n + i) * a.Hq + kvh * a.G + r % a.G) * D;
   if (!valid || len == 0) {
-    if (threadIdx.x < D) out[threadIdx.x] = valid ? (T)0.f : (T)__uint_as_float(0x7fffffffu);
+    for (int d = part_of * 32 + lane; d < D; d += 32 * WPR) out[d] = valid ? (T)0.f : (T)__uint_as_float(0x7fffffffu);
     return;
   }
   if (c0 == c1) return;
@@ -759,9 +756,9 @@ __global__ void __launch_bounds__(kThreads) q8_join_kernel(const Q8AttendArgs a,
   float gl = kLowest, gv = kLowest, sum = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (uint32_t b = c0 + warp; b <= c1; b += 32 * kWarps) {
-    const uint32_t c = b + kWarps * lane;                  // this lane's CTA
-    const int n = (int)min(32u, (c1 - b) / kWarps + 1);
+  for (uint32_t b = c0 + part_of; b <= c1; b += 32 * WPR) {
+    const uint32_t c = b + WPR * lane;                     // this lane's CTA
+    const int n = (int)min(32u, (c1 - b) / WPR + 1);
     float ml = kLowest, mv = kLowest, l = 0.f;
     if (lane < n) {
       const float4 x = *reinterpret_cast<const float4*>(part + (size_t)(c * 2 + (c == c0 ? slot0 : 0)) * S::ROWS * S::OROW + D);
@@ -782,7 +779,7 @@ __global__ void __launch_bounds__(kThreads) q8_join_kernel(const Q8AttendArgs a,
       float p[8][E];
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
-        const uint32_t cx = min(b + kWarps * (x0 + x), c1 - (c1 - b) % kWarps);
+        const uint32_t cx = min(b + WPR * (x0 + x), c1 - (c1 - b) % WPR);
         const float* src = part + (size_t)(cx * 2 + (cx == c0 ? slot0 : 0)) * S::ROWS * S::OROW + E * lane;
         if (E == 4) {
           const float4 v = *reinterpret_cast<const float4*>(src);
@@ -801,10 +798,16 @@ __global__ void __launch_bounds__(kThreads) q8_join_kernel(const Q8AttendArgs a,
       }
     }
   }
+  if (WPR == 1) {
+    const float c = sum == 0.f ? 0.f : ex2(gv - gl) / sum;   // no token: 0
+#pragma unroll
+    for (int e = 0; e < E; e += 2) reinterpret_cast<uint32_t*>(out)[(E * lane + e) / 2] = pack16<T>(o[e] * c, o[e + 1] * c);
+    return;
+  }
   if (lane == 0) wm[warp][0] = gl, wm[warp][1] = gv, wm[warp][2] = sum;
 #pragma unroll
   for (int e = 0; e < E; ++e) wo[warp][E * lane + e] = o[e];
-  __syncthreads();
+  __syncthreads();                                         // WPR is kWarps: one row a block
   if (threadIdx.x >= D) return;
   gl = gv = kLowest, sum = 0.f;
   float t = 0.f;
@@ -815,12 +818,12 @@ __global__ void __launch_bounds__(kThreads) q8_join_kernel(const Q8AttendArgs a,
     sum += wm[w][2] * ex2(wm[w][0] - gl);
     t += wo[w][threadIdx.x] * ex2(wm[w][1] - gv);
   }
-  out[threadIdx.x] = (T)result(t, gl, gv, sum);
+  out[threadIdx.x] = (T)(sum == 0.f ? 0.f : t * (ex2(gv - gl) / sum));
 }
 
 // A unit's query rows are cut into passes of up to 24, as even as eights allow.  24 rows are what registers
 // hold: a pass of 32 spilled, and took 81 us (int8, fp16) and 123 us (e4m3, bf16) for 8 queries of 4 heads over 16
-// rows of 4096 tokens (8 kv heads of 128), where two passes of 16 take @@.
+// rows of 4096 tokens (8 kv heads of 128), where two passes of 16 took 78 and 75.
 int pick_nt(int rows) {
   const int eights = (rows + 7) / 8, passes = (eights + 2) / 3;
   return (eights + passes - 1) / passes;
@@ -854,8 +857,15 @@ cudaError_t launch(const Q8AttendArgs& a, uint32_t grid, cudaStream_t s) {
   }
   e = launch_dependent(kernel, dim3(grid), kThreads, smem_bytes<D, NT>(a.c.batch), s, a);
   if (e != cudaSuccess) return e;
-  return launch_dependent(q8_join_kernel<T, D, NT>, dim3((unsigned)(a.c.num_kv_heads * a.n * a.G), (unsigned)a.c.batch),
-                          kThreads, 4 * (2 * a.c.batch + 1), s, a, grid);
+  // A warp per query row where units have some 16 partial results at most: 8 queries of 4 heads in 16 rows of 4096
+  // take 69 us so, 78 with four warps a row.  Else four: a row of 131583 tokens takes 53.3 us so, 57.0 with one.
+  const int rows = a.c.num_kv_heads * a.n * a.G, units = a.c.batch * a.c.num_kv_heads * groups_of(a.c, a.Hq, a.n);
+  const int join_smem = 4 * (2 * a.c.batch + 1);
+  if ((int64_t)units * 16 >= grid)
+    return launch_dependent(q8_join_kernel<T, D, NT, 1>, dim3((unsigned)((rows + kWarps - 1) / kWarps), (unsigned)a.c.batch),
+                            kThreads, join_smem, s, a, grid);
+  return launch_dependent(q8_join_kernel<T, D, NT, kWarps>, dim3((unsigned)rows, (unsigned)a.c.batch), kThreads, join_smem,
+                          s, a, grid);
 }
 
 template <typename T, int FMT, int D>

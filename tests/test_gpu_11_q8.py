@@ -455,31 +455,35 @@ def test_append_padded_beyond_the_capacity():
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 def test_offsets_beyond_32_bits(fmt):
     """The last of 40 rows of 2^20 tokens, its codes 5 GB behind the first's,
-    beside a cache of that row alone: the same split, the same bits."""
+    beside a like cache that holds it in its first row: the same plan, the same
+    bits."""
     b, cap, d = 40, 2 ** 20, 128
-    big, one = (tq.TQ8Cache(x, 1, d, cap, fmt) for x in (b, 1))
+    last, first = (tq.TQ8Cache(b, 1, d, cap, fmt) for _ in range(2))
+    where = ((last, b - 1), (first, 0))
     g = torch.Generator("cuda").manual_seed(0)
     for w in "kv":
         raw = torch.randint(0, 120, (cap, d), generator=g, dtype=torch.uint8, device="cuda")
-        for c in (big, one):
-            getattr(c, w + "_codes")[-1, 0].view(torch.uint8).copy_(raw)
-            getattr(c, w + "_scales")[-1, 0] = torch.linspace(0.5, 2.0, cap // 64, device="cuda") / 50
+        for c, r in where:
+            getattr(c, w + "_codes")[r, 0].view(torch.uint8).copy_(raw)
+            getattr(c, w + "_scales")[r, 0] = torch.linspace(0.5, 2.0, cap // 64, device="cuda") / 50
             getattr(c, w + "_recent").fill_(0.25)
     n = cap - 70
-    lens = torch.zeros(b, **INT)
-    lens[-1] = n
-    k, v = values(1, (b, 1, 65, d), "fp16").cuda(), values(2, (b, 1, 65, d), "fp16").cuda()
-    big.append(k, v, lens, torch.tensor([0] * (b - 1) + [65], **INT))
-    one.append(k[-1:], v[-1:], lens[-1:])
-    lens[-1] += 65
-    q = values(3, (b, 2, 4, d), "fp16", False).cuda()
-    out = big.attention(q, lens)
-    assert torch.equal(out[-1:], one.attention(q[-1:], lens[-1:])) and not out[:-1].any() and out[-1].isfinite().all()
-    for x, y in zip(big.read(lens, n - 100, 165), one.read(lens[-1:], n - 100, 165)):
-        assert torch.equal(x[-1:], y) and not x[:-1].any()
-    for x in ("k_codes", "v_codes", "k_scales", "v_scales", "k_recent", "v_recent"):
-        assert torch.equal(getattr(big, x)[-1].view(torch.uint8), getattr(one, x)[-1].view(torch.uint8)), x
-    assert big.get_status() == 0 and one.get_status() == 0
+    k, v = values(1, (1, 1, 65, d), "fp16").cuda(), values(2, (1, 1, 65, d), "fp16").cuda()
+    q = values(3, (1, 2, 4, d), "fp16", False).cuda()
+    got = []
+    for c, r in where:
+        lens, rows = torch.zeros(b, **INT), torch.zeros(b, **INT)
+        lens[r], rows[r] = n, 65
+        c.append(k.expand(b, -1, -1, -1), v.expand(b, -1, -1, -1), lens, rows)
+        lens[r] += 65
+        out = c.attention(q.expand(b, -1, -1, -1), lens)
+        x = c.read(lens, n - 100, 165)
+        others = [i for i in range(b) if i != r]
+        assert out[r].isfinite().all() and not out[others].any() and not any(y[others].any() for y in x)
+        assert c.get_status() == 0
+        got.append([out[r], x[0][r], x[1][r], *[getattr(c, y)[r].view(torch.uint8) for y in
+                    ("k_codes", "v_codes", "k_scales", "v_scales", "k_recent", "v_recent")]])
+    assert all(torch.equal(x, y) for x, y in zip(*got))
 
 
 # ---- norm and rotation ------------------------------------------------------------
