@@ -15,6 +15,12 @@
 // latency, the open block's, the join of the warps).  A unit inside one CTA's
 // run is finished there; the others leave partial results that a second
 // kernel joins in a fixed order.
+//
+// One query per row is bound by HBM: 8 rows of 32768 tokens (32/8 heads of
+// 128, e4m3) take 90 to 95 us on the device, 5.7 to 6.0 TB/s, and the kernel
+// without its arithmetic as long.  Several queries are bound by the chain of
+// dependent instructions at 8 warps per SM: 5 queries in each of 16 ragged
+// rows up to 4109 tokens take 26 us where the bytes would take 8.
 #include <atomic>
 #include <cmath>
 
@@ -24,6 +30,8 @@ namespace tq {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
+// Stages of a warp's ring.  Two keep 48 KB per SM on their way, what HBM's latency asks for; with three, or with four
+// CTAs per SM, 8 rows of 32K tokens take 102 us instead of 94 (more outstanding reads make HBM slower).
 constexpr int kStages = 2;
 constexpr float kLowest = -3.0e38f;          // of a reference before its first token
 constexpr float kShift = 7.f;                // numerator weights are 2^7 at their reference (mv holds it less 7),
@@ -84,7 +92,8 @@ __device__ __forceinline__ bool row_valid(const Q8AttendArgs& a, int len, int nr
   return len >= 0 && len <= a.c.capacity && nr >= 0 && nr <= a.n;
 }
 // What a unit costs besides its tiles, in tiles.  Measured: 33 ragged rows with one query each (NT = 1) take
-// 45 us with 8 and 54 with 4; 5 queries in each of 16 rows (NT = 3, heavier tiles) 33.5 with 8 and 31.6 with 4.
+// 43.3 us with 8, 45.6 with 6, 51.8 with 4; 5 queries in each of 16 rows (NT = 3, heavier tiles) 28.4 with 8, 26.4
+// with 4, 27.4 with 3.
 constexpr int unit_cost(int nt) { return nt == 1 ? 8 : 4; }
 // In shared memory: places before each row [batch + 1], lengths [batch] (0 where a row has no work).
 struct Plan {
@@ -137,7 +146,7 @@ __device__ __forceinline__ void plan_rows(const Q8AttendArgs& a, int subs, int c
   __syncthreads();
 }
 // A run has one place at least: with few, short rows the tiles' latency is what counts (a row of 1536 tokens with 4
-// kv heads: 7.3 us with one place a CTA, 7.8 with two, 8.8 with four).
+// kv heads: 6.7 us with one place a CTA, 7.3 with two, 8.3 with four).
 __device__ __forceinline__ uint32_t plan_ctas(uint32_t places, uint32_t grid) { return places < grid ? places : grid; }
 // Runs of places / ctas places, one more in the first ones.
 struct Runs {
@@ -223,7 +232,8 @@ struct Shape {
   static_assert(NT <= kWarps);                             // a warp brings eight of them
   static constexpr int Q = QS ? NT * (D / 16) * 256 + ROWS * 4 : 0;
 };
-// CTAs per SM: what registers and shared memory allow.
+// CTAs per SM: what registers and shared memory allow (two queries' passes of d = 64 with three instead of two: 17.9
+// us instead of 19.1 for 8 rows of 8192).
 constexpr int ctas_per_sm(int d, int nt) { return nt == 1 ? (d == 128 ? 3 : 4) : nt == 2 && d == 64 ? 3 : 2; }
 template <int D, int NT>
 int smem_bytes(int batch) {
