@@ -5,7 +5,11 @@
 //   x_p = sigma log2(e) s_k <q, c_k>,   o = sum_p 2^x_p s_v c_v / sum_p 2^x_p
 // in one pass, with two running references: ml of x for the denominator, and
 // mv of x + log2 s_v for the numerator, whose weights 2^(x + log2 s_v - mv)
-// take the place of an fp16 operand without a multiplication by s_v.
+// take the place of an fp16 operand without a multiplication by s_v.  That
+// rounding (2^-11 of a weight) is the one that the arithmetic adds: codes and
+// fp16 values are exact operands, sums and references float32, and the
+// weights' errors average over the tokens, so that a result's own rounding to
+// 16 bits is the larger one.
 //
 // The work is the batch's tiles (a unit's whole blocks of 64 tokens, then its
 // open block), flattened and cut into equal runs, one per CTA, so that rows of
@@ -293,7 +297,9 @@ struct Pass {
       }
   }
   // ... in fp16: a bf16 query is scaled by the power of two that brings its
-  // largest element into [1, 2); returns sigma log2(e) by that power.
+  // largest element into [1, 2) (elements below 2^-14 of it lose at most 2^-25
+  // of it, under float32's own rounding of the sum); returns sigma log2(e) by
+  // that power.
   __device__ __forceinline__ float half_q(const Q8AttendArgs& a, uint32_t (&f)[KS][2]) {
     if (!Pair16<T>::kWide) return a.scale_log2;
     uint32_t mx = 0;

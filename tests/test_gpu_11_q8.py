@@ -486,6 +486,63 @@ def test_offsets_beyond_32_bits(fmt):
     assert all(torch.equal(x, y) for x, y in zip(*got))
 
 
+def test_nothing_to_attend_to():
+    """All rows empty: zeros; no queries in any row: out as it was."""
+    for b in (3, 40):
+        st = Stream(b, 2, 64, 128, "int8", "fp16")
+        q = values(84, (b, 2, 4, 64), "fp16", False).cuda()
+        out = st.c.attention(q, st.lens(), out=torch.full_like(q, 5.0))
+        assert not out.any()
+        st.append(85, 100)
+        out = st.c.attention(q, st.lens(), torch.zeros(b, **INT), out=torch.full_like(q, 5.0))
+        assert (out == 5).all() and st.c.get_status() == 0
+
+
+def test_append_strides_of_their_own_and_another_stream():
+    """k token by token, v head by head, on a side stream; a broadcast head."""
+    st = Stream(2, 3, 64, 256, "e4m3", "fp16")
+    k, v = values(86, (2, 70, 3, 64), "fp16"), values(87, (2, 3, 70, 64), "fp16")
+    side = torch.cuda.Stream()
+    kd, vd, lens = k.cuda(), v.cuda(), st.lens()
+    torch.cuda.synchronize()
+    st.c.append(kd.transpose(1, 2), vd, lens, stream=side)
+    for w, t in (("k", k.transpose(1, 2)), ("v", v)):
+        st.x[w] = list(t)
+    st.len = [70, 70]
+    side.synchronize()
+    st.check()
+    out = st.c.read(torch.tensor(st.len, **INT), 60, 10, stream=side)
+    side.synchronize()
+    assert torch.equal(out[0][:, :, 4:].cpu(), k.transpose(1, 2)[:, :, 64:]) and torch.equal(out[1][:, :, 4:].cpu(), v[:, :, 64:])
+    one = kd[:, :, :1].transpose(1, 2).expand(-1, 3, -1, -1)
+    st.c.append(one, one, lens)
+    assert all(torch.equal(st.c.k_recent[:, h, 64:70], kd[:, 64:, 0]) for h in range(3))
+
+
+def test_a_cache_takes_over_buffers():
+    a = Stream(2, 2, 64, 256, "int8", "bf16")
+    a.append(88, 100, [100, 33])
+    names = [w + x for w in "kv" for x in ("_codes", "_scales", "_recent")]
+    b = Stream.__new__(Stream)
+    b.__dict__.update(a.__dict__)
+    b.c = tq.TQ8Cache(2, 2, 64, 256, "int8", torch.bfloat16, buffers={x: getattr(a.c, x) for x in names})
+    b.append(89, 90, [90, 31])
+    b.check()
+    run_attention(b, 90, 2, 4)
+    assert all(getattr(a.c, x) is getattr(b.c, x) for x in names)
+
+
+def test_norm_rope_on_another_stream():
+    qkv = values(92, (2, 5, 8, 64), "fp16").cuda()
+    pos, f = torch.arange(5, **INT).expand(2, 5).contiguous(), torch.linspace(0, 1, 32, device="cuda")
+    want = tq.qk_norm_rope(qkv[:, :, :4], qkv[:, :, 4:], pos, f)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = tq.qk_norm_rope(qkv[:, :, :4], qkv[:, :, 4:], pos, f, stream=side)
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+
+
 # ---- norm and rotation ------------------------------------------------------------
 
 def rope_bound(y, x, weight, dtype):
