@@ -51,21 +51,19 @@ cudaError_t sm_count(int* sms) {
 
 extern "C" {
 
-tq_status tq_q8_append(const tq_q8_cache* c, const void* k, const void* v, int64_t k_row_stride,
-                       int64_t k_head_stride, int64_t k_token_stride, int64_t v_row_stride,
-                       int64_t v_head_stride, int64_t v_token_stride, int32_t n,
-                       const int32_t* lens, const int32_t* n_rows, cudaStream_t stream) {
+tq_status tq_q8_append(const tq_q8_cache* c, const tq_q8_append_args* x, cudaStream_t stream) {
   const tq_status st = check_cache(c);
   if (st != TQ_OK) return st;
-  if (n < 0) return TQ_ERR_INVALID_ARG;
-  if (n == 0) return TQ_OK;
-  if (!k || !v || !lens || !aligned(k, 16) || !aligned(v, 16) || !aligned(lens, 4) || !aligned(n_rows, 4) ||
-      !good_stride(k_row_stride) || !good_stride(k_head_stride) || !good_stride(k_token_stride) ||
-      !good_stride(v_row_stride) || !good_stride(v_head_stride) || !good_stride(v_token_stride))
+  if (!x || x->n < 0) return TQ_ERR_INVALID_ARG;
+  if (x->n == 0) return TQ_OK;
+  if (!x->k || !x->v || !x->lens || !aligned(x->k, 16) || !aligned(x->v, 16) || !aligned(x->lens, 4) ||
+      !aligned(x->n_rows, 4) || !good_stride(x->k_row_stride) || !good_stride(x->k_head_stride) ||
+      !good_stride(x->k_token_stride) || !good_stride(x->v_row_stride) || !good_stride(x->v_head_stride) ||
+      !good_stride(x->v_token_stride))
     return TQ_ERR_INVALID_ARG;
-  if (n > c->capacity && !n_rows) return TQ_ERR_CAPACITY;
-  const Q8AppendArgs a{*c, {k, v}, {k_row_stride, v_row_stride}, {k_head_stride, v_head_stride},
-                       {k_token_stride, v_token_stride}, n, lens, n_rows};
+  if (x->n > c->capacity && !x->n_rows) return TQ_ERR_CAPACITY;
+  const Q8AppendArgs a{*c, {x->k, x->v}, {x->k_row_stride, x->v_row_stride}, {x->k_head_stride, x->v_head_stride},
+                       {x->k_token_stride, x->v_token_stride}, x->n, x->lens, x->n_rows};
   return launch_q8_append(a, stream) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
@@ -94,24 +92,22 @@ tq_status tq_q8_attention_bytes(const tq_q8_cache* c, int32_t num_q_heads, int32
   return TQ_OK;
 }
 
-tq_status tq_q8_attention(const tq_q8_cache* c, const void* q, int64_t row_stride, int64_t token_stride,
-                          int64_t head_stride, int32_t num_q_heads, int32_t n, const int32_t* lens,
-                          const int32_t* n_rows, float softmax_scale, void* out, void* scratch,
-                          size_t scratch_bytes, cudaStream_t stream) {
+tq_status tq_q8_attention(const tq_q8_cache* c, const tq_q8_attention_args* x, cudaStream_t stream) {
   tq_status st = check_cache(c);
   if (st != TQ_OK) return st;
-  if (!q || !lens || !out || !scratch || !aligned(q, 16) || !aligned(out, 16) || !aligned(lens, 4) ||
-      !aligned(n_rows, 4) || !aligned(scratch, 256) || !good_stride(row_stride) || !good_stride(token_stride) ||
-      !good_stride(head_stride) || !std::isfinite(softmax_scale))
+  if (!x || !x->q || !x->lens || !x->out || !x->scratch || !aligned(x->q, 16) || !aligned(x->out, 16) ||
+      !aligned(x->lens, 4) || !aligned(x->n_rows, 4) || !aligned(x->scratch, 256) || !good_stride(x->row_stride) ||
+      !good_stride(x->token_stride) || !good_stride(x->head_stride) || !std::isfinite(x->softmax_scale))
     return TQ_ERR_INVALID_ARG;
-  st = check_attention(c, num_q_heads, n);
+  st = check_attention(c, x->num_q_heads, x->n);
   if (st != TQ_OK) return st;
   int sms;
   if (sm_count(&sms) != cudaSuccess) return TQ_ERR_CUDA;
-  if (scratch_bytes < q8_attend_scratch(*c, num_q_heads, n, sms)) return TQ_ERR_INVALID_ARG;
-  const double sigma = softmax_scale == 0.f ? 1.0 / std::sqrt((double)c->head_dim) : (double)softmax_scale;
-  const Q8AttendArgs a{*c, q, row_stride, token_stride, head_stride, num_q_heads, num_q_heads / c->num_kv_heads,
-                       n, lens, n_rows, (float)(sigma * 1.4426950408889634), out, (uint8_t*)scratch};
+  if (x->scratch_bytes < q8_attend_scratch(*c, x->num_q_heads, x->n, sms)) return TQ_ERR_INVALID_ARG;
+  const double sigma = x->softmax_scale == 0.f ? 1.0 / std::sqrt((double)c->head_dim) : (double)x->softmax_scale;
+  const Q8AttendArgs a{*c, x->q, x->row_stride, x->token_stride, x->head_stride, x->num_q_heads,
+                       x->num_q_heads / c->num_kv_heads, x->n, x->lens, x->n_rows,
+                       (float)(sigma * 1.4426950408889634), x->out, (uint8_t*)x->scratch};
   return launch_q8_attend(a, sms, stream) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
@@ -124,29 +120,27 @@ tq_status tq_q8_get_status(const tq_q8_cache* c, cudaStream_t stream) {
   return w & kQ8StatusCapacity ? TQ_ERR_CAPACITY : w ? TQ_ERR_INVALID_ARG : TQ_OK;
 }
 
-tq_status tq_qk_norm_rope(int32_t batch, int32_t n, int32_t num_q_heads, int32_t num_kv_heads,
-                          int32_t head_dim, int32_t dtype, const void* q, int64_t q_row_stride,
-                          int64_t q_token_stride, int64_t q_head_stride, const void* k, int64_t k_row_stride,
-                          int64_t k_token_stride, int64_t k_head_stride, const int32_t* positions,
-                          const float* inv_freq, const void* q_weight, const void* k_weight, float eps,
-                          int32_t interleaved, void* q_out, void* k_out, cudaStream_t stream) {
-  if (batch < 0 || n < 0 || num_q_heads < 0 || num_kv_heads < 0 || head_dim < 1 ||
-      (dtype != TQ_DTYPE_FP16 && dtype != TQ_DTYPE_BF16) || (interleaved != 0 && interleaved != 1) ||
-      !(eps >= 0.f) || std::isinf(eps))
+tq_status tq_qk_norm_rope(const tq_qk_norm_rope_args* x, cudaStream_t stream) {
+  if (!x || x->batch < 0 || x->n < 0 || x->num_q_heads < 0 || x->num_kv_heads < 0 || x->head_dim < 1 ||
+      (x->dtype != TQ_DTYPE_FP16 && x->dtype != TQ_DTYPE_BF16) || (x->interleaved != 0 && x->interleaved != 1) ||
+      !(x->eps >= 0.f) || std::isinf(x->eps))
     return TQ_ERR_INVALID_ARG;
-  if (head_dim != 64 && head_dim != 128) return TQ_ERR_UNSUPPORTED;
-  if ((int64_t)num_q_heads + num_kv_heads > 65535 || (int64_t)batch * n > INT_MAX) return TQ_ERR_UNSUPPORTED;
-  if (batch == 0 || n == 0 || num_q_heads + num_kv_heads == 0) return TQ_OK;
-  if (!positions || !inv_freq || !aligned(positions, 4) || !aligned(inv_freq, 4)) return TQ_ERR_INVALID_ARG;
-  if (num_q_heads > 0 && (!q || !q_out || !aligned(q, 16) || !aligned(q_out, 16) || !aligned(q_weight, 16) ||
-                          !good_stride(q_row_stride) || !good_stride(q_token_stride) || !good_stride(q_head_stride)))
+  if (x->head_dim != 64 && x->head_dim != 128) return TQ_ERR_UNSUPPORTED;
+  if ((int64_t)x->num_q_heads + x->num_kv_heads > 65535 || (int64_t)x->batch * x->n > INT_MAX) return TQ_ERR_UNSUPPORTED;
+  if (x->batch == 0 || x->n == 0 || x->num_q_heads + x->num_kv_heads == 0) return TQ_OK;
+  if (!x->positions || !x->inv_freq || !aligned(x->positions, 4) || !aligned(x->inv_freq, 4)) return TQ_ERR_INVALID_ARG;
+  if (x->num_q_heads > 0 &&
+      (!x->q || !x->q_out || !aligned(x->q, 16) || !aligned(x->q_out, 16) || !aligned(x->q_weight, 16) ||
+       !good_stride(x->q_row_stride) || !good_stride(x->q_token_stride) || !good_stride(x->q_head_stride)))
     return TQ_ERR_INVALID_ARG;
-  if (num_kv_heads > 0 && (!k || !k_out || !aligned(k, 16) || !aligned(k_out, 16) || !aligned(k_weight, 16) ||
-                           !good_stride(k_row_stride) || !good_stride(k_token_stride) || !good_stride(k_head_stride)))
+  if (x->num_kv_heads > 0 &&
+      (!x->k || !x->k_out || !aligned(x->k, 16) || !aligned(x->k_out, 16) || !aligned(x->k_weight, 16) ||
+       !good_stride(x->k_row_stride) || !good_stride(x->k_token_stride) || !good_stride(x->k_head_stride)))
     return TQ_ERR_INVALID_ARG;
-  const NormRopeArgs a{batch, n, num_q_heads, num_kv_heads, head_dim, dtype, q, k, q_row_stride, q_token_stride,
-                       q_head_stride, k_row_stride, k_token_stride, k_head_stride, positions, inv_freq, q_weight,
-                       k_weight, eps, interleaved, q_out, k_out};
+  const NormRopeArgs a{x->batch, x->n, x->num_q_heads, x->num_kv_heads, x->head_dim, x->dtype, x->q, x->k,
+                       x->q_row_stride, x->q_token_stride, x->q_head_stride, x->k_row_stride, x->k_token_stride,
+                       x->k_head_stride, x->positions, x->inv_freq, x->q_weight, x->k_weight, x->eps, x->interleaved,
+                       x->q_out, x->k_out};
   return launch_norm_rope(a, stream) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 

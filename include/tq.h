@@ -437,7 +437,8 @@ tq_status tq_export_vectors(tq_vec_index* index, const void* codes, int64_t star
  * head, block) for K and one for V.  It has no host-side state: lengths are
  * device arrays that the caller advances, so every call can be captured in
  * a CUDA graph and replayed as the rows grow, and the layers of a model
- * share one array.
+ * share one array.  Calls with many arguments take them in a struct, which is
+ * read before the call returns.
  *
  * What is held.  Position p of a row belongs to block p / 64.  Of a row of
  * length L, the tokens of its floor(L / 64) whole blocks are read from the
@@ -490,10 +491,16 @@ typedef struct tq_q8_cache {
  * as it was and TQ_ERR_INVALID_ARG is latched in the status word; a row
  * that would exceed the capacity likewise, with TQ_ERR_CAPACITY.
  */
-tq_status tq_q8_append(const tq_q8_cache* cache, const void* k, const void* v,
-                       int64_t k_row_stride, int64_t k_head_stride, int64_t k_token_stride,
-                       int64_t v_row_stride, int64_t v_head_stride, int64_t v_token_stride,
-                       int32_t n, const int32_t* lens, const int32_t* n_rows, cudaStream_t stream);
+typedef struct tq_q8_append_args {
+  const void* k;
+  const void* v;
+  int64_t k_row_stride, k_head_stride, k_token_stride;
+  int64_t v_row_stride, v_head_stride, v_token_stride;
+  int32_t n;
+  const int32_t* lens;
+  const int32_t* n_rows;
+} tq_q8_append_args;
+tq_status tq_q8_append(const tq_q8_cache* cache, const tq_q8_append_args* args, cudaStream_t stream);
 
 /*
  * Read positions start .. start + n - 1 of every row back to 16 bits.
@@ -538,11 +545,19 @@ tq_status tq_q8_attention_bytes(const tq_q8_cache* cache, int32_t num_q_heads, i
  * outputs NaN that attend to it and no others.  Lengths and n_rows out of
  * range are latched as TQ_ERR_INVALID_ARG, and the row's outputs are NaN.
  */
-tq_status tq_q8_attention(const tq_q8_cache* cache, const void* q, int64_t row_stride,
-                          int64_t token_stride, int64_t head_stride, int32_t num_q_heads,
-                          int32_t n, const int32_t* lens, const int32_t* n_rows,
-                          float softmax_scale, void* out, void* scratch, size_t scratch_bytes,
-                          cudaStream_t stream);
+typedef struct tq_q8_attention_args {
+  const void* q;
+  int64_t row_stride, token_stride, head_stride;
+  int32_t num_q_heads;
+  int32_t n;
+  const int32_t* lens;
+  const int32_t* n_rows;
+  float softmax_scale;
+  void* out;
+  void* scratch;
+  size_t scratch_bytes;
+} tq_q8_attention_args;
+tq_status tq_q8_attention(const tq_q8_cache* cache, const tq_q8_attention_args* args, cudaStream_t stream);
 
 /* Synchronize `stream`, then return and clear the latched status: TQ_OK,
  * TQ_ERR_CAPACITY or TQ_ERR_INVALID_ARG. */
@@ -570,13 +585,22 @@ tq_status tq_q8_get_status(const tq_q8_cache* cache, cudaStream_t stream);
  * Outputs must not overlap inputs.  num_q_heads or num_kv_heads may be 0
  * (its pointers are then not used).
  */
-tq_status tq_qk_norm_rope(int32_t batch, int32_t n, int32_t num_q_heads, int32_t num_kv_heads,
-                          int32_t head_dim, int32_t dtype, const void* q, int64_t q_row_stride,
-                          int64_t q_token_stride, int64_t q_head_stride, const void* k,
-                          int64_t k_row_stride, int64_t k_token_stride, int64_t k_head_stride,
-                          const int32_t* positions, const float* inv_freq, const void* q_weight,
-                          const void* k_weight, float eps, int32_t interleaved, void* q_out,
-                          void* k_out, cudaStream_t stream);
+typedef struct tq_qk_norm_rope_args {
+  int32_t batch, n, num_q_heads, num_kv_heads, head_dim, dtype;
+  const void* q;
+  int64_t q_row_stride, q_token_stride, q_head_stride;
+  const void* k;
+  int64_t k_row_stride, k_token_stride, k_head_stride;
+  const int32_t* positions;
+  const float* inv_freq;
+  const void* q_weight;
+  const void* k_weight;
+  float eps;
+  int32_t interleaved;
+  void* q_out;
+  void* k_out;
+} tq_qk_norm_rope_args;
+tq_status tq_qk_norm_rope(const tq_qk_norm_rope_args* args, cudaStream_t stream);
 
 /*
  * Measurement hook: when `start` and `stop` are non-NULL, every following

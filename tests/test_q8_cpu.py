@@ -1,6 +1,7 @@
 """The 8-bit cache on the CPU: pins of its oracle by closed forms and worked
 values, and the library's refusals, which come before any device call."""
 import ctypes
+import struct
 
 import numpy as np
 import pytest
@@ -111,6 +112,23 @@ def test_norm_rope_closed_forms(interleaved):
     assert abs(t[0, 0, 1 if interleaved else 4] - 1) < 1e-15
 
 
+# The argument structs, fields in the order of include/tq.h; None is NULL.
+def _pack(fmt, *fields):
+    return struct.pack(fmt, *[0 if x is None else x for x in fields])
+
+
+def _append(lib, ref, *f):
+    return lib.tq_q8_append(ref, _pack("@PP6qi4xPP", *f[:-1]), f[-1])
+
+
+def _attention(lib, ref, *f):
+    return lib.tq_q8_attention(ref, _pack("@P3q2iPPf4xPPN", *f[:-1]), f[-1])
+
+
+def _norm_rope(lib, *f):
+    return lib.tq_qk_norm_rope(_pack("@6iP3qP3q4Pfi2P", *f[:-1]), f[-1])
+
+
 # ---- refusals ---------------------------------------------------------------
 
 def _struct(**kw):
@@ -134,17 +152,24 @@ def test_every_call_refuses_a_bad_cache(lib, kw, code):
     c = _struct(**kw)
     r = ctypes.addressof(c)
     size = ctypes.c_size_t()
-    assert lib.tq_q8_append(r, 256, 256, 8, 8, 8, 8, 8, 8, 1, 256, None, None) == code
+    assert _append(lib, r, 256, 256, 8, 8, 8, 8, 8, 8, 1, 256, None, None) == code
     assert lib.tq_q8_read(r, 256, 0, 1, 256, 256, None) == code
-    assert lib.tq_q8_attention(r, 256, 8, 8, 8, 4, 1, 256, None, 0.0, 256, 256, 1 << 40, None) == code
+    assert _attention(lib, r, 256, 8, 8, 8, 4, 1, 256, None, 0.0, 256, 256, 1 << 40, None) == code
     if not any(k in kw for k in ("k_codes", "v_codes", "k_scales", "v_recent", "status")):
         assert lib.tq_q8_attention_bytes(r, 4, 1, ctypes.byref(size)) == code
 
 
+def test_null_structs(lib):
+    r = ctypes.addressof(c := _struct())
+    assert lib.tq_q8_append(r, None, None) == 1 and lib.tq_q8_attention(r, None, None) == 1
+    assert lib.tq_qk_norm_rope(None, None) == 1
+    del c
+
+
 def test_null_cache(lib):
-    assert lib.tq_q8_append(None, 256, 256, 8, 8, 8, 8, 8, 8, 1, 256, None, None) == 1
+    assert _append(lib, None, 256, 256, 8, 8, 8, 8, 8, 8, 1, 256, None, None) == 1
     assert lib.tq_q8_read(None, 256, 0, 1, 256, 256, None) == 1
-    assert lib.tq_q8_attention(None, 256, 8, 8, 8, 4, 1, 256, None, 0.0, 256, 256, 1 << 40, None) == 1
+    assert _attention(lib, None, 256, 8, 8, 8, 4, 1, 256, None, 0.0, 256, 256, 1 << 40, None) == 1
     assert lib.tq_q8_attention_bytes(None, 4, 1, None) == 1
     assert lib.tq_q8_get_status(None, None) == 1
 
@@ -155,7 +180,7 @@ def test_null_cache(lib):
 def test_append_refusals(lib, at, value, code):
     args = [ctypes.addressof(c := _struct()), 256, 256, 8, 8, 8, 8, 8, 8, 1, 256, None, None]
     args[at] = value
-    assert lib.tq_q8_append(*args) == code
+    assert _append(lib, *args) == code
     del c
 
 
@@ -175,7 +200,7 @@ def test_read_refusals(lib, at, value, code):
 def test_attention_refusals(lib, at, value, code):
     args = [ctypes.addressof(c := _struct()), 256, 8, 8, 8, 4, 1, 256, None, 0.0, 256, 256, 1 << 40, None]
     args[at] = value
-    assert lib.tq_q8_attention(*args) == code
+    assert _attention(lib, *args) == code
     del c
 
 
@@ -187,7 +212,7 @@ def test_attention_refusals(lib, at, value, code):
 def test_norm_rope_refusals(lib, at, value, code):
     args = [1, 1, 4, 2, 64, 0, 256, 8, 8, 8, 256, 8, 8, 8, 256, 256, 256, 256, 1e-6, 0, 256, 256, None]
     args[at] = value
-    assert lib.tq_qk_norm_rope(*args) == code
+    assert _norm_rope(lib, *args) == code
 
 
 @pytest.mark.parametrize("kw", [dict(format="int4"), dict(dtype=torch.float32), dict(capacity=100), dict(head_dim=96),
