@@ -34,7 +34,8 @@
  *    only the host-side handle (freed by tq_cache_destroy).  Input buffers
  *    are borrowed until the stream-ordered work that reads them completes.
  *  - Streams: every device call is asynchronous on the given stream and
- *    never synchronizes, except tq_get_status and the tq_export_* helpers.
+ *    never synchronizes, except the tq_*get_status calls and the tq_export_*
+ *    helpers.
  *  - Errors: argument, shape and capacity errors are returned synchronously
  *    before any launch, and leave the handle unchanged.  Launch failures
  *    return TQ_ERR_CUDA.  Conditions detected on the device (an fp16 scale
@@ -462,7 +463,7 @@ tq_status tq_export_vectors(tq_vec_index* index, const void* codes, int64_t star
 
 typedef struct tq_q8_cache {
   int32_t batch;            /* rows B, 1..1024                               */
-  int32_t num_kv_heads;     /* Hkv >= 1                                      */
+  int32_t num_kv_heads;     /* Hkv >= 1, B Hkv <= 65535                      */
   int32_t head_dim;         /* d: 64 or 128                                  */
   int32_t format;           /* TQ_Q8_INT8 or TQ_Q8_E4M3                      */
   int32_t dtype;            /* of inputs, outputs and ring: TQ_DTYPE_*       */
@@ -523,7 +524,8 @@ tq_status tq_q8_attention_bytes(const tq_q8_cache* cache, int32_t num_q_heads, i
  * Attention of the newest n tokens of every row over the row's cache.
  *   q        device 16-bit [B, n, Hq, d] by strides of the row, the token
  *            and the head (as for tq_q8_append); Hq a multiple of Hkv with
- *            Hq / Hkv <= 16, 1 <= n <= 64
+ *            Hq / Hkv <= 16, 1 <= n <= 64; query head h reads kv head
+ *            h / (Hq / Hkv)
  *   lens     device int32 [B]: tokens that row b holds, the n newest (those
  *            of q) among them
  *   n_rows   device int32 [B] or NULL: row b has n_rows[b] <= n queries; what

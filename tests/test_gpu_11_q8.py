@@ -221,8 +221,10 @@ def test_rejected_drafts_are_set_back():
         st.append(1, 150)
         st.append(2, back + 3)
         st.len[0] -= back
+        run_attention(st, 4, 2, 4)
         st.append(3, 100)
         st.check()
+        run_attention(st, 5, 2, 4)
 
 
 def test_append_refuses_rows_on_the_device():
@@ -659,6 +661,44 @@ def test_a_decoding_run_captured_and_replayed():
     check_attention(st, q, out[1])
 
 
+def test_a_forked_capture():
+    """A captured step whose calls lie on two streams, after a copy and beside
+    other work: rotation and append on one, a memset between them."""
+    b, hq, h, d, n = 2, 8, 2, 64, 30
+    st = Stream(b, h, d, 512, "int8", "fp16")
+    st.append(95, 200, [200, 90])
+    qkv = values(96, (b, n, hq + 2 * h, d), "fp16").cuda()
+    f = torch.linspace(0, 1, d // 2, device="cuda")
+    x, pos, lens, after = torch.empty_like(qkv), torch.arange(n, **INT).expand(b, n).contiguous(), st.lens(), st.lens() + n
+    names = [w + y for w in "kv" for y in ("_codes", "_scales", "_recent")]
+
+    def step(side):
+        main = torch.cuda.current_stream()
+        x.copy_(qkv)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            q, k = tq.qk_norm_rope(x[:, :, :hq], x[:, :, hq:hq + h], pos, f)
+            pad = torch.zeros(1 << 16, device="cuda")
+            st.c.append(k, x[:, :, hq + h:].transpose(1, 2), lens)
+        busy = x.float().sum()
+        main.wait_stream(side)
+        return st.c.attention(q, after), busy, pad, q, k
+
+    side = torch.cuda.Stream()
+    want = step(side)[0].clone()
+    torch.cuda.synchronize()
+    held = {y: getattr(st.c, y).clone() for y in names}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        keep = step(side)
+    for _ in range(5):
+        keep[0].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(keep[0], want)
+        assert all(torch.equal(getattr(st.c, y).view(torch.uint8), t.view(torch.uint8)) for y, t in held.items())
+
+
 def test_two_graphs_and_an_eager_call_at_once():
     """Calls on one cache from two graphs and the current stream, replayed side
     by side: each has its own scratch."""
@@ -709,4 +749,31 @@ def test_the_compressed_cache_takes_the_rotated_keys():
                                v[i, u].double().cpu().numpy())
             assert (rel_err(got[i, hs], o[0]) <= ATTN_RTOL).all()
             assert (rel_err(got8[i, hs], o[0]) <= ATTN_RTOL).all()
+    cache.close()
+
+
+def test_rotated_queries_go_straight_into_the_compressed_decode():
+    """tq_decode_attention's first kernel reads q before it waits for the
+    kernel before it, which here is the one that writes q: 100 steps without a
+    wait give the bits of the same steps with one after every call."""
+    b, hq, h, d = 8, 32, 8, 128
+    cache = tq.TQCache(tq.make_config(b, hq, h, d, 64, 64, 3, 3, 128))
+    kv = values(97, (2, b, h, 64, d), "fp16", False).cuda()
+    cache.evict_window(kv[0].contiguous(), kv[1].contiguous())
+    qkv = values(98, (100, b, 1, hq + h, d), "fp16", False).cuda()
+    f = torch.linspace(0, 1, d // 2, device="cuda")
+    q, k = torch.empty(b, 1, hq, d, dtype=torch.float16, device="cuda"), torch.empty(b, h, 1, d, dtype=torch.float16, device="cuda")
+    pos = torch.full((b, 1), 77, **INT)
+    outs = []
+    for wait in (True, False):
+        out = torch.empty(100, b, hq, d, device="cuda")
+        for i, x in enumerate(qkv):
+            tq.qk_norm_rope(x[:, :, :hq], x[:, :, hq:], pos, f, q_out=q, k_out=k)
+            if wait:
+                torch.cuda.synchronize()
+            cache.decode_attention(q[:, 0], out=out[i])
+            if wait:
+                torch.cuda.synchronize()
+        outs.append(out)
+    assert cache.get_status() == 0 and torch.equal(*outs)
     cache.close()
