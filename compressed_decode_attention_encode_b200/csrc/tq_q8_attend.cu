@@ -5,11 +5,12 @@
 //   x_p = sigma log2(e) s_k <q, c_k>,   o = sum_p 2^x_p s_v c_v / sum_p 2^x_p
 // in one pass, with two running references: ml of x for the denominator, and
 // mv of x + log2 s_v for the numerator, whose weights 2^(x + log2 s_v - mv)
-// take the place of an fp16 operand without a multiplication by s_v.  That
-// rounding (2^-11 of a weight) is the one that the arithmetic adds: codes and
-// fp16 values are exact operands, sums and references float32, and the
-// weights' errors average over the tokens, so that a result's own rounding to
-// 16 bits is the larger one.
+// take the place of an fp16 operand without a multiplication by s_v.  Codes
+// and fp16 values are exact operands, sums and references float32.  A weight
+// rounded to fp16 (2^-11) would show beside an fp16 result's own rounding
+// where many tokens of either sign weigh alike (1.6 times its error), so fp16
+// caches take weights in two fp16 parts, at most 5 % of the time; beside a bf16 result (2^-8) it does not, so bf16 caches take
+// one (their open block two bf16 parts).
 //
 // The work is the batch's tiles (a unit's whole blocks of 64 tokens, then its
 // open block), flattened and cut into equal runs, one per CTA, so that rows of
@@ -24,7 +25,7 @@
 // 128, e4m3) take 90 to 95 us on the device, 5.7 to 6.0 TB/s, and the kernel
 // without its arithmetic as long.  Several queries are bound by the chain of
 // dependent instructions at 8 warps per SM: 5 queries in each of 16 ragged
-// rows up to 4109 tokens take 26 us where the bytes would take 8.
+// rows up to 4109 tokens take 27 us where the bytes would take 8.
 #include <atomic>
 #include <cmath>
 
@@ -266,6 +267,7 @@ template <typename T, int FMT, int D, int NT>
 struct Pass {
   using S = Shape<D, NT>;
   static constexpr int KS = D / 16;          // k-steps of the first product, m-tiles of the second
+  static constexpr int PARTS = Pair16<T>::kWide ? 1 : 2;   // of a weight, for whole blocks
   float o[KS][NT][4];                        // dims 2 mt, 2 mt + 1 of the lane's D / 8, queries 2 tig, 2 tig + 1
   float ml[NT][2], mv[NT][2], l[NT][2];
   float cq[NT][2];                           // sigma log2(e) of the query (and its power of two)
@@ -410,10 +412,25 @@ struct Pass {
       }
   }
 
+  // The next 16-bit part of the weights as the second product's operand; what
+  // it leaves stays in w.
+  template <typename P>
+  __device__ __forceinline__ void split(float (&w)[NT][4], uint32_t (&b)[NT][2]) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t pk = pack16<P>(w[t][2 * e], w[t][2 * e + 1]);
+        b[t][e] = movmatrix(pk);
+        const float2 r = unpack16<P>(pk);
+        w[t][2 * e] -= r.x, w[t][2 * e + 1] -= r.y;
+      }
+  }
+
   // The warp's 16 tokens of a tile: of a whole block, from the ring stage at
   // `st` with the scales behind it, or of the open block, from the 16-bit
   // ring in global memory.  The open block's products take the cache's own
-  // type, exactly; bf16 weights go in as two bf16 parts.
+  // type, exactly, and two parts of the weights.
   __device__ __forceinline__ void tile(const Q8AttendArgs& a, const uint8_t* st, int tile, bool open, int row, int kvh,
                                        int len) {
     constexpr int SLAB = S::SLAB;
@@ -487,12 +504,9 @@ struct Pass {
     }
     weights(s, f, lsv, first, open || (tile + 1) * kQ8Block > base + (int)((uint32_t)r0 * inv_g >> 16));
     if (!open) {
-      uint32_t b[NT][2];
+      uint32_t b[PARTS][NT][2];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        b[t][0] = movmatrix(pack16<__half>(s[t][0], s[t][1]));
-        b[t][1] = movmatrix(pack16<__half>(s[t][2], s[t][3]));
-      }
+      for (int part = 0; part < PARTS; ++part) split<__half>(s, b[part]);
       uint32_t v[4][D / 32];                               // tokens 2 tig, 2 tig + 1, + 8, + 9
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -515,7 +529,10 @@ struct Pass {
           codes_to_half4<FMT>(lo, a0, a1);
           codes_to_half4<FMT>(hi, a2, a3);
 #pragma unroll
-          for (int t = 0; t < NT; ++t) mma16816(o[2 * x + y][t], a0, a1, a2, a3, b[t][0], b[t][1], __half());
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part)
+              mma16816(o[2 * x + y][t], a0, a1, a2, a3, b[part][t][0], b[part][t][1], __half());
         }
     } else {
       bad = __reduce_or_sync(~0u, bad);
@@ -533,17 +550,9 @@ struct Pass {
             if ((bad >> (gid + 8 * (e >> 1)) & 1) && first + gid + 8 * (e >> 1) < end_of(t, e & 1)) s[t][e] = NAN;
       }
 #pragma unroll
-      for (int part = 0; part < (Pair16<T>::kWide ? 2 : 1); ++part) {
+      for (int part = 0; part < 2; ++part) {
         uint32_t b[NT][2];
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t pk = pack16<T>(s[t][2 * e], s[t][2 * e + 1]);
-            b[t][e] = movmatrix(pk);
-            const float2 r = unpack16<T>(pk);
-            s[t][2 * e] -= r.x, s[t][2 * e + 1] -= r.y;
-          }
+        split<T>(s, b);
 #pragma unroll
         for (int x = 0; x < KS; ++x) {
           const uint32_t v0 = word(vo[0][x / 4], x % 4), v1 = word(vo[1][x / 4], x % 4);

@@ -540,7 +540,7 @@ tq_status tq_q8_attention_bytes(const tq_q8_cache* cache, int32_t num_q_heads, i
  *   out = sum_p softmax_p(sigma <q, k_p>) v_p
  * and is zero where there is none.  Sums and softmax statistics are float32;
  * the products take fp16 operands, which hold codes and fp16 values exactly,
- * and the weights rounded once.  The same call gives the same bits; how a row
+ * and the weights in two parts (bf16 caches: one).  The same call gives the same bits; how a row
  * is split over the card, and so the order of its sums, follows the lengths
  * of all rows.
  * A token that holds a NaN or an infinity, or whose block does, makes the
