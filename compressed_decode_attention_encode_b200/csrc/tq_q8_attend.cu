@@ -9,8 +9,9 @@
 // and fp16 values are exact operands, sums and references float32.  A weight
 // rounded to fp16 (2^-11) would show beside an fp16 result's own rounding
 // where many tokens of either sign weigh alike (1.6 times its error), so fp16
-// caches take weights in two fp16 parts, at most 5 % of the time; beside a bf16 result (2^-8) it does not, so bf16 caches take
-// one (their open block two bf16 parts).
+// caches take weights in two fp16 parts, at most 5 % of the time; beside a
+// bf16 result (2^-8) it does not, so bf16 caches take one (their open block
+// two bf16 parts).
 //
 // The work is the batch's tiles (a unit's whole blocks of 64 tokens, then its
 // open block), flattened and cut into equal runs, one per CTA, so that rows of
