@@ -6,12 +6,12 @@
 // in one pass, with two running references: ml of x for the denominator, and
 // mv of x + log2 s_v for the numerator, whose weights 2^(x + log2 s_v - mv)
 // take the place of an fp16 operand without a multiplication by s_v.  Codes
-// and fp16 values are exact operands, sums and references float32.  A weight
-// rounded to fp16 (2^-11) would show beside an fp16 result's own rounding
-// where many tokens of either sign weigh alike (1.6 times its error), so fp16
-// caches take weights in two fp16 parts, at most 5 % of the time; beside a
-// bf16 result (2^-8) it does not, so bf16 caches take one (their open block
-// two bf16 parts).
+// and fp16 values are exact operands, sums and references float32.  Weights
+// enter the second product in parts that leave float32's own precision: two of
+// fp16 (2^-22), in a bf16 cache's open block three of bf16 (2^-24).  With one
+// fp16 part, which saved 0 to 5 %, the error beside an fp16 result's own
+// rounding was 1.6 times as large where many tokens of either sign weigh
+// alike, and one bf16 result in twenty was rounded to the neighbour.
 //
 // The work is the batch's tiles (a unit's whole blocks of 64 tokens, then its
 // open block), flattened and cut into equal runs, one per CTA, so that rows of
@@ -268,7 +268,7 @@ template <typename T, int FMT, int D, int NT>
 struct Pass {
   using S = Shape<D, NT>;
   static constexpr int KS = D / 16;          // k-steps of the first product, m-tiles of the second
-  static constexpr int PARTS = Pair16<T>::kWide ? 1 : 2;   // of a weight, for whole blocks
+  static constexpr int PARTS = 2, OPEN_PARTS = Pair16<T>::kWide ? 3 : 2;   // of a weight: for whole blocks, for the open one
   float o[KS][NT][4];                        // dims 2 mt, 2 mt + 1 of the lane's D / 8, queries 2 tig, 2 tig + 1
   float ml[NT][2], mv[NT][2], l[NT][2];
   float cq[NT][2];                           // sigma log2(e) of the query (and its power of two)
@@ -431,7 +431,7 @@ struct Pass {
   // The warp's 16 tokens of a tile: of a whole block, from the ring stage at
   // `st` with the scales behind it, or of the open block, from the 16-bit
   // ring in global memory.  The open block's products take the cache's own
-  // type, exactly, and two parts of the weights.
+  // type, exactly, and the weights in parts of it.
   __device__ __forceinline__ void tile(const Q8AttendArgs& a, const uint8_t* st, int tile, bool open, int row, int kvh,
                                        int len) {
     constexpr int SLAB = S::SLAB;
@@ -551,7 +551,7 @@ struct Pass {
             if ((bad >> (gid + 8 * (e >> 1)) & 1) && first + gid + 8 * (e >> 1) < end_of(t, e & 1)) s[t][e] = NAN;
       }
 #pragma unroll
-      for (int part = 0; part < 2; ++part) {
+      for (int part = 0; part < OPEN_PARTS; ++part) {
         uint32_t b[NT][2];
         split<T>(s, b);
 #pragma unroll

@@ -540,9 +540,9 @@ tq_status tq_q8_attention_bytes(const tq_q8_cache* cache, int32_t num_q_heads, i
  *   out = sum_p softmax_p(sigma <q, k_p>) v_p
  * and is zero where there is none.  Sums and softmax statistics are float32;
  * the products take fp16 operands, which hold codes and fp16 values exactly,
- * and the weights in two parts (bf16 caches: one).  The same call gives the same bits; how a row
- * is split over the card, and so the order of its sums, follows the lengths
- * of all rows.
+ * and the weights in parts that leave 2^-22 of them.  The same call gives the
+ * same bits; how a row is split over the card, and so the order of its sums,
+ * follows the lengths of all rows.
  * A token that holds a NaN or an infinity, or whose block does, makes the
  * outputs NaN that attend to it and no others.  Lengths and n_rows out of
  * range are latched as TQ_ERR_INVALID_ARG, and the row's outputs are NaN.
