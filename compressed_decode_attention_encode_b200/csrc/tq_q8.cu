@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kRopeThreads, 5) norm_rope_kernel(const NormRo
     if (own != weight && own) wt[0] = reinterpret_cast<const uint4*>(own)[lane], wt[1] = reinterpret_cast<const uint4*>(own)[lane + L];
     weight = own;
   };
-  weigh(use.keys);
+  if (use.h < use.heads) weigh(use.keys);                  // a lane may have no head at all
 #pragma unroll
   for (int i = 0; i < D / 64; ++i) {
     const int p = tid % 32 + 32 * i;

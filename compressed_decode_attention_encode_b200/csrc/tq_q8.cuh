@@ -66,6 +66,18 @@ struct NormRopeArgs {
   void* k_out;
 };
 
+// The kernel's arguments: what belongs to a side without heads is not used, so
+// nothing of it goes on.
+inline NormRopeArgs norm_rope_args(const tq_qk_norm_rope_args& x) {
+  NormRopeArgs a{x.batch, x.n, x.num_q_heads, x.num_kv_heads, x.head_dim, x.dtype, x.q, x.k,
+                 x.q_row_stride, x.q_token_stride, x.q_head_stride, x.k_row_stride, x.k_token_stride,
+                 x.k_head_stride, x.positions, x.inv_freq, x.q_weight, x.k_weight, x.eps, x.interleaved,
+                 x.q_out, x.k_out};
+  if (x.num_q_heads == 0) a.q = a.q_weight = a.q_out = nullptr, a.q_row = a.q_token = a.q_head = 0;
+  if (x.num_kv_heads == 0) a.k = a.k_weight = a.k_out = nullptr, a.k_row = a.k_token = a.k_head = 0;
+  return a;
+}
+
 cudaError_t launch_q8_append(const Q8AppendArgs& a, cudaStream_t s);
 cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s);
 size_t q8_attend_scratch(const tq_q8_cache& c, int Hq, int n, int num_sms);

@@ -137,10 +137,7 @@ tq_status tq_qk_norm_rope(const tq_qk_norm_rope_args* x, cudaStream_t stream) {
       (!x->k || !x->k_out || !aligned(x->k, 16) || !aligned(x->k_out, 16) || !aligned(x->k_weight, 16) ||
        !good_stride(x->k_row_stride) || !good_stride(x->k_token_stride) || !good_stride(x->k_head_stride)))
     return TQ_ERR_INVALID_ARG;
-  const NormRopeArgs a{x->batch, x->n, x->num_q_heads, x->num_kv_heads, x->head_dim, x->dtype, x->q, x->k,
-                       x->q_row_stride, x->q_token_stride, x->q_head_stride, x->k_row_stride, x->k_token_stride,
-                       x->k_head_stride, x->positions, x->inv_freq, x->q_weight, x->k_weight, x->eps, x->interleaved,
-                       x->q_out, x->k_out};
+  const NormRopeArgs a = norm_rope_args(*x);
   return launch_norm_rope(a, stream) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 

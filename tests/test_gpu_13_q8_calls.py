@@ -1,0 +1,26 @@
+"""Calls that the 8-bit cache's contracts allow, beside the ordinary ones."""
+import numpy as np
+import pytest
+import torch
+
+from compressed_decode_attention_encode_b200 import tq
+from oracle import q8_oracle as O
+from tests.test_gpu_11_q8 import INT, rope_bound, values
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("hq,h", [(3, 0), (0, 3), (1, 0), (0, 1), (5, 0), (0, 5)])
+def test_norm_rope_of_one_side_with_its_weight(hq, h, dtype, d):
+    """Queries alone or keys alone, whose heads leave lanes of a warp idle."""
+    x = values(100, (2, 3, hq + h, d), dtype).cuda()
+    w = values(101, (d,), dtype, False).cuda()
+    pos, f = torch.arange(6, **INT).view(2, 3), torch.linspace(0, 1, d // 2, device="cuda")
+    q_out, k_out = tq.qk_norm_rope(x[:, :, :hq], x[:, :, hq:], pos, f, w if hq else None, w if h else None, eps=1e-5)
+    got = (q_out if hq else k_out.transpose(1, 2)).double().cpu().numpy()
+    xs, ws = x.double().cpu().numpy(), w.double().cpu().numpy()
+    want = O.norm_rope(xs, pos.cpu().numpy(), f.cpu().numpy(), ws, 1e-5)
+    flat = O.norm_rope(xs, np.zeros((2, 3)), f.cpu().numpy(), ws, 1e-5)
+    assert (np.abs(got - want) <= rope_bound(want, flat, ws, dtype)).all()
