@@ -438,8 +438,10 @@ tq_status tq_export_vectors(tq_vec_index* index, const void* codes, int64_t star
  * head, block) for K and one for V.  It has no host-side state: lengths are
  * device arrays that the caller advances, so every call can be captured in
  * a CUDA graph and replayed as the rows grow, and the layers of a model
- * share one array.  Calls with many arguments take them in a struct, which is
- * read before the call returns.
+ * share one array.  Host threads may call at the same time; what is written
+ * by one call and used by another is ordered by their streams, as always.
+ * Calls with many arguments take them in a struct, which is read before the
+ * call returns.
  *
  * What is held.  Position p of a row belongs to block p / 64.  Of a row of
  * length L, the tokens of its floor(L / 64) whole blocks are read from the
@@ -535,7 +537,8 @@ tq_status tq_q8_attention_bytes(const tq_q8_cache* cache, int32_t num_q_heads, i
  *   softmax_scale  sigma; 0 selects 1/sqrt(d)
  *   scratch  device, 256-byte aligned, at least tq_q8_attention_bytes; it
  *            holds nothing between calls, and calls whose GPU work overlaps
- *            need one each
+ *            need one each (calls on one stream do not overlap, whatever host
+ *            threads they come from)
  * Query i of row b attends to its positions below lens[b] - n_rows[b] + 1 + i:
  *   out = sum_p softmax_p(sigma <q, k_p>) v_p
  * and is zero where there is none.  Sums and softmax statistics are float32;

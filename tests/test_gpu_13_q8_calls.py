@@ -1,11 +1,13 @@
 """Calls that the 8-bit cache's contracts allow, beside the ordinary ones."""
+import threading
+
 import numpy as np
 import pytest
 import torch
 
 from compressed_decode_attention_encode_b200 import tq
 from oracle import q8_oracle as O
-from tests.test_gpu_11_q8 import INT, rope_bound, values
+from tests.test_gpu_11_q8 import INT, Stream, rope_bound, values
 
 pytestmark = pytest.mark.gpu
 
@@ -24,3 +26,28 @@ def test_norm_rope_of_one_side_with_its_weight(hq, h, dtype, d):
     want = O.norm_rope(xs, pos.cpu().numpy(), f.cpu().numpy(), ws, 1e-5)
     flat = O.norm_rope(xs, np.zeros((2, 3)), f.cpu().numpy(), ws, 1e-5)
     assert (np.abs(got - want) <= rope_bound(want, flat, ws, dtype)).all()
+
+
+def test_threads_share_a_cache_and_a_stream():
+    """Calls of several host threads on one cache, one stream and one scratch,
+    each with units that many CTAs share: every one gives what it gives alone."""
+    st = Stream(1, 2, 128, 8192, "int8", "fp16")
+    st.append(110, 8100)
+    lens = st.lens()
+    qs = [values(111 + i, (1, 1 + i, 8, 128), "fp16", False).cuda() for i in range(4)]
+    want = [st.c.attention(q, lens) for q in qs]
+    scratch = torch.empty(max(st.c.scratch_bytes(8, 1 + i) for i in range(4)), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    wrong = [None] * 4
+
+    def calls(i):
+        outs = [st.c.attention(qs[i], lens, scratch=s) for _ in range(200) for s in (None, scratch)]
+        torch.cuda.synchronize()
+        wrong[i] = sum(not torch.equal(o, want[i]) for o in outs)
+
+    threads = [threading.Thread(target=calls, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert wrong == [0] * 4 and st.c.get_status() == 0
