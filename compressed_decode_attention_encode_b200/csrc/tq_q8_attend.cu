@@ -42,6 +42,7 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kStages = 2;
 constexpr float kLowest = -3.0e38f;          // of a reference before its first token
 constexpr float kShift = 7.f;                // numerator weights are 2^7 at their reference (mv holds it less 7),
+constexpr float kNothing = -1000.f;          // in place of log2 s_v where the codes are zeros: moves no reference
 constexpr float kLazy = 8.f;                 // and a reference moves when one exceeds it by 2^8: below fp16's 2^16
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -447,7 +448,20 @@ struct Pass {
       for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
     if (!open) {
       const float sk = *reinterpret_cast<const float*>(st + 2 * SLAB);
-      lsv = lg2(*reinterpret_cast<const float*>(st + 2 * SLAB + 4));
+      const float sv = *reinterpret_cast<const float*>(st + 2 * SLAB + 4);
+      lsv = lg2(sv);
+      if (sv == 1.f) {
+        // A block of zeros has this scale.  Its tokens add nothing to the numerator, and its reference would leave
+        // the weights of later blocks with small values below what fp16 holds.
+        uint32_t any = 0;
+#pragma unroll
+        for (int i = 0; i < SLAB / 512; ++i) {
+          const uint4 v = *reinterpret_cast<const uint4*>(st + SLAB + 512 * i + 16 * lane);
+          any |= v.x | v.y | v.z | v.w;
+        }
+        if (FMT == TQ_Q8_E4M3) any &= 0x7f7f7f7fu;         // -0 is a zero
+        if (!__any_sync(~0u, any)) lsv = kNothing;
+      }
 #pragma unroll
       for (int t = 0; t < NT; ++t) f[t][0] = sk * cq[t][0], f[t][1] = sk * cq[t][1];
 #pragma unroll

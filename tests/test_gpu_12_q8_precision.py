@@ -15,31 +15,41 @@ from tests.test_gpu_11_q8 import DT, Stream, values
 pytestmark = pytest.mark.gpu
 
 
-def float32_bound(w, q, ck, sk, cv, sv, sigma):
+def float32_bound(w, q, ck, sk, cv, sv, sigma, dtype, alike=False):
     """|error| [n, G, d] of a result before it is rounded to its type.  With
     A = sum_p w_p |v_p|:
 
     * a logit sums as many exact products as q has elements that are not zero,
       each addition off by at most 2^-23 of sum |q k|, with four roundings
-      around it; an error e of a logit changes a weight by 2 e (its exponential
-      and the denominator's);
+      around it; bf16 queries enter as fp16 after a power of two, elements below
+      2^-31 of the largest off by 2^-40 of it; an error e of a logit changes a
+      weight by 2 e (its exponential and the denominator's).  ``alike``: the
+      logits that count are computed from the same numbers, e = 0;
     * a weight in two fp16 parts is off by 2^-11 of 2^-11; exponentials by
       2^-22 each, of the weight, of a reference's move, of the join and of the
       result's factor; a block's scale, as a logarithm, by 2^-22 of it;
     * sums: (L / 16 + 64) additions of 2^-23;
     * a weight's last fp16 part ends at 2^-25, where the row's largest
-      w_p scale_p stands at 2^7 or above, times |code|.
+      w_p scale_p so far stands at 2^7 or above, times the code.  Blocks of
+      zeros count for nothing; the open block comes last, with scale 1.
     """
     v = cv * sv[:, None]
-    length = len(sv)
+    length, whole = len(sv), len(sv) // 64 * 64
+    top = np.abs(v).max(-1)
+    for j in range(0, length, 64):
+        top[j:j + 64] = top[j:j + 64].max()
+    scale = np.where(top > 0, sv, 0.0)
+    ref = (w * scale)[..., :whole].max(-1, initial=0.0)[..., None]
+    last = np.maximum(ref, w[..., whole:].max(-1, initial=0.0)[..., None])
     qk = np.einsum("ngd,ld->ngl", np.abs(q), np.abs(ck)) * sk * abs(sigma)
-    e = ((np.count_nonzero(q, axis=-1)[..., None] + 4) * 2.0 ** -23 * qk).max(-1)[..., None]
+    e = (np.count_nonzero(q, axis=-1)[..., None] + 4) * 2.0 ** -23 * qk
+    if dtype == "bf16":
+        e = e + 2.0 ** -40 * np.abs(q).max(-1)[..., None] * (np.abs(ck).sum(-1) * sk * abs(sigma))
+    e = 0.0 if alike else e.max(-1)[..., None]
     a = w @ np.abs(v)
-    live = sv[np.abs(cv).max(-1) > 0]
-    logs = np.abs(np.log2(live)).max() if len(live) else 0.0
-    ref = (w * sv).max(-1)[..., None]
+    logs = np.abs(np.log2(scale[:whole][top[:whole] > 0])).max(initial=0.0)
     return (a * (2 * e + 2.0 ** -22 * (5 + logs) + (length / 16 + 64) * 2.0 ** -23)
-            + 2.0 ** -32 * ref * np.abs(cv).sum(0))
+            + 2.0 ** -32 * (ref * np.abs(cv[:whole]).sum(0) + last * np.abs(cv[whole:]).sum(0)))
 
 
 def half_step(x, dtype):
@@ -49,23 +59,29 @@ def half_step(x, dtype):
     return np.ldexp(t.eps / 2, e - 1)
 
 
-def assert_rounded(st, q, out, rows=None, sigma=0.0):
-    """Every result of rows is the oracle's, rounded, but for float32_bound."""
+def assert_rounded(st, q, out, rows=None, sigma=0.0, alike=False, only=None):
+    """Every result of rows (of those in ``only``) is the oracle's, rounded, but for float32_bound."""
     b, h, d = st.shape
     n, hq = q.shape[1:3]
     g = hq // h
     got, qd = out.double().cpu().numpy(), q.double().cpu().numpy()
     sig = sigma or 1 / math.sqrt(d)
-    for i in range(b):
+    for i in range(b) if only is None else only:
         r = n if rows is None else rows[i]
         for u in range(h):
             heads = slice(u * g, (u + 1) * g)
             (ck, sk), (cv, sv) = ((c[u], s[u]) for c, s in (st.stored("k", i), st.stored("v", i)))
             o, w = O.attention(qd[i, :r, heads], ck * sk[:, None], cv * sv[:, None], sig)
-            lim = float32_bound(w, qd[i, :r, heads], ck, sk, cv, sv, sig)
+            lim = float32_bound(w, qd[i, :r, heads], ck, sk, cv, sv, sig, st.dtype, alike)
             over = np.abs(got[i, :r, heads] - o) - half_step(np.abs(o) + lim, st.dtype) - lim
             assert (over <= 0).all(), (i, u, int((over > 0).sum()), float((over / lim).max()))
     assert st.c.get_status() == 0
+
+
+def single(b, n, hq, d, dtype, value):
+    """Queries of one element each, another one in every head."""
+    q = torch.zeros(b, n, hq, d, dtype=DT[dtype])
+    return q.scatter_(3, torch.arange(b * n * hq).view(b, n, hq, 1) % d, value).cuda()
 
 
 @pytest.mark.parametrize("d", [64, 128])
@@ -78,8 +94,42 @@ def test_a_result_is_rounded_once(fmt, dtype, d, n):
     lens = [64, 128, 63, 100, 17, 3]
     st = Stream(len(lens), 2, d, 128, fmt, dtype)
     st.append(1, max(lens), lens)
-    q = torch.zeros(len(lens), n, 16, d, dtype=DT[dtype])
-    at = torch.arange(len(lens) * n * 16).view(len(lens), n, 16, 1) % d
-    q.scatter_(3, at, 2 * math.sqrt(d))
-    q = q.cuda()
+    q = single(len(lens), n, 16, d, dtype, 2 * math.sqrt(d))
     assert_rounded(st, q, st.c.attention(q, st.lens()))
+
+
+@pytest.mark.parametrize("d,n", [(64, 1), (128, 3)])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype,size", [("bf16", 1e-6), ("bf16", 1e-8), ("bf16", 1e-28), ("fp16", 1e-6), ("fp16", 1.0)])
+def test_blocks_of_zeros_take_nothing_from_small_values(fmt, dtype, size, d, n):
+    """Whole blocks of small values between blocks of zeros, whose scale is 1."""
+    b = 240                                                 # so many that a unit's tiles lie in one CTA's run
+    st = Stream(b, 2, d, 320, fmt, dtype)
+    k, v = values(3, (3, 320, 2, d), dtype), (values(4, (3, 320, 2, d), dtype).float() * size).to(DT[dtype])
+    v[:, 64:128], v[1, :64], v[2, 256:] = 0, -1e-39, 0      # what is below 2^-100 is stored as zeros, of either sign
+    st.append(0, 320, k=k.repeat(b // 3, 1, 1, 1), v=v.repeat(b // 3, 1, 1, 1))
+    q = single(b, n, 16, d, dtype, 2 * math.sqrt(d))
+    assert_rounded(st, q, st.c.attention(q, st.lens()), only=[0, 1, 2, 118, 239])
+
+
+def test_only_zeros():
+    st = Stream(3, 2, 64, 192, "int8", "bf16")
+    k = values(5, (3, 190, 2, 64), "bf16")
+    st.append(0, 190, [190, 128, 30], k=k, v=torch.zeros_like(k))
+    assert not st.c.attention(single(3, 2, 8, 64, "bf16", 16.0), st.lens()).any()
+
+
+@pytest.mark.parametrize("d,n", [(64, 1), (128, 3)])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype,size", [("bf16", 1e-6), ("bf16", 1e-8), ("bf16", 1e-28), ("bf16", 1e-38), ("bf16", 1e30),
+                                        ("fp16", 1e-6), ("fp16", 1e-3), ("fp16", 500.0)])
+def test_the_open_block_takes_nothing_from_small_values(fmt, dtype, size, d, n):
+    """Small and large values in whole blocks and the open one, whose values
+    are their own codes; one warp's share of the open block is zeros."""
+    b = 240                                                 # so many that a unit's tiles lie in one CTA's run
+    st = Stream(b, 2, d, 320, fmt, dtype)
+    k, v = values(6, (3, 249, 2, d), dtype), (values(7, (3, 249, 2, d), dtype, False).float() * size).to(DT[dtype])
+    v[:, 208:224] = 0
+    st.append(0, 249, [249, 192, 40] * (b // 3), k=k.repeat(b // 3, 1, 1, 1), v=v.repeat(b // 3, 1, 1, 1))
+    q = single(b, n, 16, d, dtype, 2 * math.sqrt(d))
+    assert_rounded(st, q, st.c.attention(q, st.lens()), only=[0, 1, 2, 118, 239])
