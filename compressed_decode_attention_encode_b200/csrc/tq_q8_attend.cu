@@ -302,9 +302,10 @@ struct Pass {
       }
   }
   // ... in fp16: a bf16 query is scaled by the power of two that brings its
-  // largest element into [1, 2) (elements below 2^-14 of it lose at most 2^-25
-  // of it, under float32's own rounding of the sum); returns sigma log2(e) by
-  // that power.
+  // largest element into [2^14, 2^15), so that elements down to 2^-31 of it are
+  // exact and those below lose at most 2^-40 of it; returns sigma log2(e) by
+  // that power.  (With the largest element in [1, 2) these were 2^-17 and
+  // 2^-25, which showed where the largest elements meet keys of zero.)
   __device__ __forceinline__ float half_q(const Q8AttendArgs& a, uint32_t (&f)[KS][2]) {
     if (!Pair16<T>::kWide) return a.scale_log2;
     uint32_t mx = 0;
@@ -313,7 +314,7 @@ struct Pass {
     mx = max(mx & 0xffffu, mx >> 16);
     mx = max(mx, __shfl_xor_sync(~0u, mx, 1));
     mx = max(mx, __shfl_xor_sync(~0u, mx, 2));
-    const int e = mx >= 0x7f80u ? 0 : min(max((int)(mx >> 7) - 127, -126), 126);   // NaN and infinities pass as they are
+    const int e = mx >= 0x7f80u ? 0 : max((int)(mx >> 7) - 127 - 14, -126);   // NaN and infinities pass as they are
     const float down = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
     for (int s = 0; s < KS; ++s)

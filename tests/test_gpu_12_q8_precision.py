@@ -133,3 +133,18 @@ def test_the_open_block_takes_nothing_from_small_values(fmt, dtype, size, d, n):
     st.append(0, 249, [249, 192, 40] * (b // 3), k=k.repeat(b // 3, 1, 1, 1), v=v.repeat(b // 3, 1, 1, 1))
     q = single(b, n, 16, d, dtype, 2 * math.sqrt(d))
     assert_rounded(st, q, st.c.attention(q, st.lens()), only=[0, 1, 2, 118, 239])
+
+
+@pytest.mark.parametrize("d,n", [(64, 1), (128, 3)])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("large", [2.0 ** 10, 2.0 ** 20, 2.0 ** 24])
+def test_a_large_query_element_takes_nothing_from_the_others(fmt, large, d, n):
+    """bf16 queries with an element that meets only zero keys."""
+    st = Stream(2, 2, d, 256, fmt, "bf16")
+    k = values(8, (2, 250, 2, d), "bf16")
+    k[..., 5] = 0
+    st.append(0, 250, [250, 130], k=k, v=values(9, (2, 250, 2, d), "bf16"))
+    q = values(10, (2, n, 16, d), "bf16", False)
+    q[..., 5] = large
+    q = q.cuda()
+    assert_rounded(st, q, st.c.attention(q, st.lens()))
