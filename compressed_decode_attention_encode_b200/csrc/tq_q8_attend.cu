@@ -4,8 +4,10 @@
 // and codes c:
 //   x_p = sigma log2(e) s_k <q, c_k>,   o = sum_p 2^x_p s_v c_v / sum_p 2^x_p
 // in one pass, with two running references: ml of x for the denominator, and
-// mv of x + log2 s_v for the numerator, whose weights 2^(x + log2 s_v - mv)
-// take the place of an fp16 operand without a multiplication by s_v.  Codes
+// ml + dv of x + log2 s_v for the numerator, whose weights
+// 2^((x - ml) + (log2 s_v - dv)) take the place of an fp16 operand without a
+// multiplication by s_v.  dv is kept as a difference because a sum x + log2 s_v
+// is rounded at x: at logits of 10^5 it left half a percent of error.  Codes
 // and fp16 values are exact operands, sums and references float32.  Weights
 // enter the second product in parts that leave float32's own precision: two of
 // fp16 (2^-22), in a bf16 cache's open block three of bf16 (2^-24).  With one
@@ -40,8 +42,8 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 // Stages of a warp's ring.  Two keep 48 KB per SM on their way, what HBM's latency asks for; with three, or with four
 // CTAs per SM, 8 rows of 32K tokens take 102 us instead of 94 (more outstanding reads make HBM slower).
 constexpr int kStages = 2;
-constexpr float kLowest = -3.0e38f;          // of a reference before its first token
-constexpr float kShift = 7.f;                // numerator weights are 2^7 at their reference (mv holds it less 7),
+constexpr float kLowest = -3.0e38f;          // ml before its first token
+constexpr float kShift = 7.f;                // numerator weights are 2^7 at their reference (dv holds it less 7),
 constexpr float kNothing = -1000.f;          // in place of log2 s_v where the codes are zeros: moves no reference
 constexpr float kLazy = 8.f;                 // and a reference moves when one exceeds it by 2^8: below fp16's 2^16
 
@@ -233,7 +235,7 @@ struct Shape {
   static constexpr int SLAB = 16 * D;                      // bytes of 16 tokens' codes
   static constexpr int STAGE = 2 * SLAB + 16;              // K, V, scales
   static constexpr int RING = kWarps * kStages * STAGE;
-  static constexpr int OROW = D + 4;                       // a row of partial results: o, ml, mv, l
+  static constexpr int OROW = D + 4;                       // a row of partial results: o, ml, dv, l
   static constexpr int JOIN = kWarps * ROWS * OROW * 4;
   static constexpr int WALK = kWarps * 2 * (int)sizeof(Walk);
   static constexpr bool QS = NT > 1;                       // queries in shared memory, not in registers
@@ -272,7 +274,7 @@ struct Pass {
   static constexpr int KS = D / 16;          // k-steps of the first product, m-tiles of the second
   static constexpr int PARTS = 2, OPEN_PARTS = Pair16<T>::kWide ? 3 : 2;   // of a weight: for whole blocks, for the open one
   float o[KS][NT][4];                        // dims 2 mt, 2 mt + 1 of the lane's D / 8, queries 2 tig, 2 tig + 1
-  float ml[NT][2], mv[NT][2], l[NT][2];
+  float ml[NT][2], dv[NT][2], l[NT][2];
   float cq[NT][2];                           // sigma log2(e) of the query (and its power of two)
   uint32_t qf[S::QS ? 1 : NT][KS][2];        // the queries' operand, or its place in shared memory
   uint2* qs;
@@ -354,8 +356,8 @@ struct Pass {
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        ml[t][j] = mv[t][j] = kLowest;
-        l[t][j] = 0.f;
+        ml[t][j] = kLowest;
+        dv[t][j] = l[t][j] = 0.f;
         cq[t][j] = !Pair16<T>::kWide ? a.scale_log2 : S::QS ? qup[8 * t + 2 * tig + j] : __shfl_sync(~0u, up, 4 * (2 * tig + j));
       }
   }
@@ -388,8 +390,8 @@ struct Pass {
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float m = fmaxf(x[t][j], x[t][j + 2]);
-        over = fmaxf(over, fmaxf(m - ml[t][j], m + (lsv - mv[t][j]) - kShift));
+        const float y = fmaxf(x[t][j], x[t][j + 2]) - ml[t][j];
+        over = fmaxf(over, fmaxf(y, y + (lsv - dv[t][j] - kShift)));
       }
     if (__any_sync(~0u, over > kLazy)) {
 #pragma unroll
@@ -399,10 +401,11 @@ struct Pass {
           float m = fmaxf(x[t][j], x[t][j + 2]);
 #pragma unroll
           for (int d = 4; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-          const float nl = fmaxf(ml[t][j], m), nv = fmaxf(mv[t][j], m + lsv - kShift);
-          l[t][j] *= ex2(ml[t][j] - nl);
-          const float c = ex2(mv[t][j] - nv);
-          ml[t][j] = nl, mv[t][j] = nv;
+          const float nl = fmaxf(ml[t][j], m), down = ml[t][j] - nl;
+          const float old = dv[t][j] + down, nv = fmaxf(old, (m - nl) + (lsv - kShift));
+          l[t][j] *= ex2(down);
+          const float c = ex2(old - nv);
+          ml[t][j] = nl, dv[t][j] = nv;
 #pragma unroll
           for (int k = 0; k < KS; ++k) o[k][t][j] *= c, o[k][t][j + 2] *= c;
         }
@@ -411,8 +414,9 @@ struct Pass {
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        l[t][e & 1] += ex2(x[t][e] - ml[t][e & 1]);
-        x[t][e] = ex2(x[t][e] + (lsv - mv[t][e & 1]));
+        const float y = x[t][e] - ml[t][e & 1];
+        l[t][e & 1] += ex2(y);
+        x[t][e] = ex2(y + (lsv - dv[t][e & 1]));
       }
   }
 
@@ -593,7 +597,7 @@ struct Pass {
         float* p = area + (warp * ROWS + 8 * t + 2 * tig + j) * OROW;
 #pragma unroll
         for (int d = 4; d < 32; d *= 2) l[t][j] += __shfl_xor_sync(~0u, l[t][j], d);
-        if (gid == 0) p[D] = ml[t][j], p[D + 1] = mv[t][j], p[D + 2] = l[t][j];
+        if (gid == 0) p[D] = ml[t][j], p[D + 1] = dv[t][j], p[D + 2] = l[t][j];
 #pragma unroll
         for (int m = 0; m < KS; m += 2)
           *reinterpret_cast<float4*>(p + D / 8 * gid + 2 * m) =
@@ -728,25 +732,26 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q8_attend_kernel
     for (int x = threadIdx.x; x < rows * (D / 4); x += kThreads) {
       const int r = x / (D / 4), d = x % (D / 4) * 4;
       const float* p = area + r * S::OROW;
-      float gl = kLowest, gv = kLowest, sum = 0.f;
+      float gl = kLowest, gv = -INFINITY, sum = 0.f;
       float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        gl = fmaxf(gl, p[w * S::ROWS * S::OROW + D]);
-        gv = fmaxf(gv, p[w * S::ROWS * S::OROW + D + 1]);
-      }
+      for (int w = 0; w < kWarps; ++w) gl = fmaxf(gl, p[w * S::ROWS * S::OROW + D]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w)
+        gv = fmaxf(gv, p[w * S::ROWS * S::OROW + D + 1] + (p[w * S::ROWS * S::OROW + D] - gl));
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float* pw = p + w * S::ROWS * S::OROW;
-        sum += pw[D + 2] * ex2(pw[D] - gl);
-        const float c = ex2(pw[D + 1] - gv);
+        const float down = pw[D] - gl;
+        sum += pw[D + 2] * ex2(down);
+        const float c = ex2(pw[D + 1] + down - gv);
         const float4 v = *reinterpret_cast<const float4*>(pw + d);
         t.x += v.x * c, t.y += v.y * c, t.z += v.z * c, t.w += v.w * c;
       }
       if (all) {
         const int i = (int)((uint32_t)(r0 + r) * ps.inv_g >> 16), h = kvh * a.G + (r0 + r) - i * a.G;
         T* out = static_cast<T*>(a.out) + (((size_t)row * a.n + i) * a.Hq + h) * D + d;
-        const float c = sum == 0.f ? 0.f : ex2(gv - gl) / sum;   // no token: 0
+        const float c = sum == 0.f ? 0.f : ex2(gv) / sum;  // no token: 0
         *reinterpret_cast<uint2*>(out) = make_uint2(pack16<T>(t.x * c, t.y * c), pack16<T>(t.z * c, t.w * c));
       } else {
         *reinterpret_cast<float4*>(part + r * S::OROW + d) = t;
@@ -795,25 +800,27 @@ __global__ void __launch_bounds__(kThreads) q8_join_kernel(const Q8AttendArgs a,
   }
   if (c0 == c1) return;
   const float* part = reinterpret_cast<const float*>(a.scratch) + (size_t)(r % S::ROWS) * S::OROW;
-  float gl = kLowest, gv = kLowest, sum = 0.f, o[E];
+  float gl = kLowest, gv = -INFINITY, sum = 0.f, o[E];      // gv relative to gl
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
   for (uint32_t b = c0 + part_of; b <= c1; b += 32 * WPR) {
     const uint32_t c = b + WPR * lane;                     // this lane's CTA
     const int n = (int)min(32u, (c1 - b) / WPR + 1);
-    float ml = kLowest, mv = kLowest, l = 0.f;
+    float ml = kLowest, dv = -INFINITY, l = 0.f;
     if (lane < n) {
       const float4 x = *reinterpret_cast<const float4*>(part + (size_t)(c * 2 + (c == c0 ? slot0 : 0)) * S::ROWS * S::OROW + D);
-      ml = x.x, mv = x.y, l = x.z;
+      ml = x.x, dv = x.y, l = x.z;
     }
-    float nl = fmaxf(gl, ml), nv = fmaxf(gv, mv);
+    float nl = fmaxf(gl, ml);
 #pragma unroll
-    for (int d = 16; d; d /= 2) nl = fmaxf(nl, __shfl_xor_sync(~0u, nl, d)), nv = fmaxf(nv, __shfl_xor_sync(~0u, nv, d));
+    for (int d = 16; d; d /= 2) nl = fmaxf(nl, __shfl_xor_sync(~0u, nl, d));
     l *= ex2(ml - nl);
+    gv += gl - nl, dv += ml - nl;
+    float nv = fmaxf(gv, dv);
 #pragma unroll
-    for (int d = 16; d; d /= 2) l += __shfl_xor_sync(~0u, l, d);
+    for (int d = 16; d; d /= 2) l += __shfl_xor_sync(~0u, l, d), nv = fmaxf(nv, __shfl_xor_sync(~0u, nv, d));
     sum = sum * ex2(gl - nl) + l;
-    const float keep = ex2(gv - nv), w = ex2(mv - nv);
+    const float keep = ex2(gv - nv), w = ex2(dv - nv);
     gl = nl, gv = nv;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] *= keep;
@@ -841,7 +848,7 @@ __global__ void __launch_bounds__(kThreads) q8_join_kernel(const Q8AttendArgs a,
     }
   }
   if (WPR == 1) {
-    const float c = sum == 0.f ? 0.f : ex2(gv - gl) / sum;   // no token: 0
+    const float c = sum == 0.f ? 0.f : ex2(gv) / sum;        // no token: 0
 #pragma unroll
     for (int e = 0; e < E; e += 2) reinterpret_cast<uint32_t*>(out)[(E * lane + e) / 2] = pack16<T>(o[e] * c, o[e + 1] * c);
     return;
@@ -851,16 +858,19 @@ __global__ void __launch_bounds__(kThreads) q8_join_kernel(const Q8AttendArgs a,
   for (int e = 0; e < E; ++e) wo[warp][E * lane + e] = o[e];
   __syncthreads();                                         // WPR is kWarps: one row a block
   if (threadIdx.x >= D) return;
-  gl = gv = kLowest, sum = 0.f;
+  gl = kLowest, gv = -INFINITY, sum = 0.f;
   float t = 0.f;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) gl = fmaxf(gl, wm[w][0]), gv = fmaxf(gv, wm[w][1]);
+  for (int w = 0; w < kWarps; ++w) gl = fmaxf(gl, wm[w][0]);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) gv = fmaxf(gv, wm[w][1] + (wm[w][0] - gl));
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    sum += wm[w][2] * ex2(wm[w][0] - gl);
-    t += wo[w][threadIdx.x] * ex2(wm[w][1] - gv);
+    const float down = wm[w][0] - gl;
+    sum += wm[w][2] * ex2(down);
+    t += wo[w][threadIdx.x] * ex2(wm[w][1] + down - gv);
   }
-  out[threadIdx.x] = (T)(sum == 0.f ? 0.f : t * (ex2(gv - gl) / sum));
+  out[threadIdx.x] = (T)(sum == 0.f ? 0.f : t * (ex2(gv) / sum));
 }
 
 // A unit's query rows are cut into passes of up to 24, as even as eights allow.  24 rows are what registers

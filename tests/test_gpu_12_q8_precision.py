@@ -148,3 +148,23 @@ def test_a_large_query_element_takes_nothing_from_the_others(fmt, large, d, n):
     q[..., 5] = large
     q = q.cuda()
     assert_rounded(st, q, st.c.attention(q, st.lens()))
+
+
+@pytest.mark.parametrize("d,n", [(64, 1), (128, 3)])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("sigma", [0.01, 1.0, 30.0, -30.0])
+def test_large_logits_that_do_not_differ(fmt, dtype, d, n, sigma):
+    """Tokens with the same key, beside one so far away that it weighs nothing:
+    the softmax is flat however large its logits are (sigma 10^6 at most)."""
+    st = Stream(4, 2, d, 8192, fmt, dtype)
+    k = torch.zeros(4, 8192, 2, d, dtype=DT[dtype])
+    k[..., 0], k[..., 1] = 100.0, 300.0
+    k[:, 70, :, 0] = -100.0 if sigma > 0 else 300.0
+    st.append(0, 8192, [64, 192, 40, 8192], k=k, v=values(11, (4, 8192, 2, d), dtype))
+    q = torch.zeros(4, n, 8, d, dtype=DT[dtype])
+    q[..., 0] = 333.0
+    q = q.cuda()
+    rows = [min(n, 1)] * 4
+    out = st.c.attention(q, st.lens(), torch.tensor(rows, dtype=torch.int32, device="cuda"), softmax_scale=sigma)
+    assert_rounded(st, q, out, rows, sigma, alike=True)
