@@ -547,7 +547,8 @@ tq_status tq_q8_attention_bytes(const tq_q8_cache* cache, int32_t num_q_heads, i
  * same bits; how a row is split over the card, and so the order of its sums,
  * follows the lengths of all rows.
  * A token that holds a NaN or an infinity, or whose block does, makes the
- * outputs NaN that attend to it and no others.  Lengths and n_rows out of
+ * outputs NaN that attend to it and no others; a query that holds one, its
+ * own outputs.  Lengths and n_rows out of
  * range are latched as TQ_ERR_INVALID_ARG, and the row's outputs are NaN.
  */
 typedef struct tq_q8_attention_args {

@@ -168,3 +168,19 @@ def test_large_logits_that_do_not_differ(fmt, dtype, d, n, sigma):
     rows = [min(n, 1)] * 4
     out = st.c.attention(q, st.lens(), torch.tensor(rows, dtype=torch.int32, device="cuda"), softmax_scale=sigma)
     assert_rounded(st, q, out, rows, sigma, alike=True)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("length", [1, 40, 64, 200, 4000])
+def test_an_infinite_query_over_keys_of_one_sign_is_no_number(dtype, length):
+    """Logits of -inf alone have no softmax; a query without tokens gives zeros."""
+    st = Stream(1, 1, 64, 4032, "int8", dtype)
+    k = torch.full((1, length, 1, 64), -1.0, dtype=DT[dtype])
+    st.append(0, length, k=k, v=values(12, (1, length, 1, 64), dtype))
+    q = torch.zeros(1, 3, 4, 64, dtype=DT[dtype])
+    q[:, :, 1, 7] = math.inf
+    q[:, :, 2, 9] = -math.inf
+    out = st.c.attention(q.cuda(), st.lens()).cpu()
+    seen = torch.tensor([length - 2, length - 1, length]) > 0
+    assert torch.isnan(out[0, seen][:, 1:3]).all() and torch.isfinite(out[0, :, [0, 3]]).all()
+    assert not out[0, ~seen].any()
