@@ -184,3 +184,26 @@ def test_an_infinite_query_over_keys_of_one_sign_is_no_number(dtype, length):
     seen = torch.tensor([length - 2, length - 1, length]) > 0
     assert torch.isnan(out[0, seen][:, 1:3]).all() and torch.isfinite(out[0, :, [0, 3]]).all()
     assert not out[0, ~seen].any()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("d,n", [(64, 1), (128, 3)])
+def test_a_flat_softmax_errs_by_its_own_rounding(fmt, d, n):
+    """fp16, 2000 tokens of either sign that weigh nearly alike: |o| is some
+    sqrt(2000) under sum w |v|, so an error of each weight shows.  Float32's
+    errors are random, sqrt(2000 / 16 + 64) of 2^-24 of that sum or 2^-15 of
+    |o|, beside the result's rounding, whose steps are 2^-11 to 2^-10 of |o|,
+    so 2^-12.8 to 2^-11.8 in the mean square: a quarter of it at most, 1.03 for
+    both together.  Weights of 11 bits err as much as the rounding does: 1.4."""
+    st = Stream(2, 2, d, 2048, fmt, "fp16")
+    st.append(13, 2000, [2000, 1920])
+    q = values(14, (2, n, 8, d), "fp16", False).cuda()
+    got = st.c.attention(q, st.lens(), softmax_scale=0.01).double().cpu().numpy()
+    err, own = 0.0, 0.0
+    for i in range(2):
+        for u in range(2):
+            (ck, sk), (cv, sv) = ((c[u], s[u]) for c, s in (st.stored("k", i), st.stored("v", i)))
+            o, _ = O.attention(q[i, :, 4 * u:4 * u + 4].double().cpu().numpy(), ck * sk[:, None], cv * sv[:, None], 0.01)
+            err += ((got[i, :, 4 * u:4 * u + 4] - o) ** 2).sum()
+            own += ((o.astype(np.float16) - o) ** 2).sum()
+    assert err <= 1.1 ** 2 * own
