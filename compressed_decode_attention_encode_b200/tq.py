@@ -520,6 +520,10 @@ def _q8_dtypes():
 
 _torch = None        # the module, once a call has needed it
 
+# Attention scratch by (device, stream): a stream's calls follow one another,
+# whatever cache or thread they come from, so the layers of a model share it.
+_scratch = {}
+
 
 def _raw_stream(torch, index: int, stream) -> int:
     """The stream to launch on: ``stream``, or PyTorch's current one of the
@@ -538,7 +542,9 @@ class TQ8Cache:
 
     The object keeps no lengths: each call takes ``lens``, an int32 tensor [B]
     on the cache's device, which the caller advances once per step for all
-    layers, so that calls can be captured in CUDA graphs.
+    layers, so that calls can be captured in CUDA graphs.  Host threads may call
+    at the same time; what one call writes and another reads is ordered by
+    their streams.
 
     ``buffers``: tensors of an earlier cache to take over, by the names
     ``k_codes``, ``v_codes`` [B, Hkv, capacity, d] (int8 or float8_e4m3fn),
@@ -581,7 +587,7 @@ class TQ8Cache:
         self._lib = lib()
         self._index = device.index if device.type == "cuda" else -1
         self._shape = (batch, num_kv_heads, head_dim)
-        self._scratch_size, self._scratch = {}, {}
+        self._scratch_size = {}
         # the sizes are checked here once, by the library (no device call)
         _check(self._lib.tq_q8_append(self._ref, _APPEND_ARGS(*[0] * 11), None), "TQ8Cache")
 
@@ -668,22 +674,23 @@ class TQ8Cache:
         return size
 
     def _take_scratch(self, size, raw):
-        """Scratch of the call: one buffer per stream, whose calls follow one
-        another; a captured call gets its own, from its graph's memory, since
-        graphs may be replayed beside anything."""
+        """Scratch of the call: one buffer per stream, for all caches; a
+        captured call gets its own, from its graph's memory, since graphs may be
+        replayed beside anything."""
         torch = self._torch
         if torch._C._cuda_isCurrentStreamCapturing():
             return torch.empty(size, dtype=torch.uint8, device=self.device)
-        t = self._scratch.get(raw)
+        key = self._index, raw
+        t = _scratch.get(key)
         if t is None or t.shape[0] < size:
-            t = self._scratch[raw] = torch.empty(size, dtype=torch.uint8, device=self.device)
+            t = _scratch[key] = torch.empty(size, dtype=torch.uint8, device=self.device)
         return t
 
     def attention(self, q, lens, n_rows=None, out=None, softmax_scale=0.0, scratch=None, stream=None):
         """q [B, n, Hq, d] (or [B, Hq, d] for one token): the newest n tokens'
         queries, attending to their row's positions up to their own; lens
         counts them.  Returns ``out`` in q's shape and type.  ``scratch``: a
-        uint8 tensor of scratch_bytes for the call (without it the object's)."""
+        uint8 tensor of scratch_bytes for the call (without it the stream's)."""
         torch = self._torch
         if stream is not None:                           # what is allocated here belongs to the call's stream
             if stream.device != self.device:

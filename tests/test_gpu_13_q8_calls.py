@@ -51,3 +51,27 @@ def test_threads_share_a_cache_and_a_stream():
     for t in threads:
         t.join()
     assert wrong == [0] * 4 and st.c.get_status() == 0
+
+
+def test_layers_share_a_streams_scratch():
+    """Twenty caches on one stream, and their calls in turn with growing
+    numbers of queries: one buffer, and every call as with scratch of its own."""
+    sts = [Stream(1, 2, 64, 4096, "int8", "fp16") for _ in range(20)]
+    for i, st in enumerate(sts):
+        st.append(120 + i, 4000 - 150 * i)
+    qs = [values(140 + i, (1, 1 + 2 * i, 8, 64), "fp16", False).cuda() for i in range(3)]
+    side = torch.cuda.Stream()
+    need = max(st.c.scratch_bytes(8, 5) for st in sts)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        outs = [torch.empty_like(q) for q in qs for _ in sts]
+        lens = [st.lens() for st in sts]
+        held = torch.cuda.memory_allocated()
+        for i, q in enumerate(qs):
+            for j, st in enumerate(sts):
+                st.c.attention(q, lens[j], out=outs[20 * i + j])
+        assert torch.cuda.memory_allocated() - held <= need + 512
+        for i, q in enumerate(qs):
+            for j, st in enumerate(sts):
+                own = torch.empty(st.c.scratch_bytes(8, 1 + 2 * i), dtype=torch.uint8, device="cuda")
+                assert torch.equal(st.c.attention(q, lens[j], scratch=own), outs[20 * i + j])
