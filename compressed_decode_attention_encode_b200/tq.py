@@ -546,6 +546,9 @@ class TQ8Cache:
     at the same time; what one call writes and another reads is ordered by
     their streams.
 
+    A row may be set back (rejected drafts) to 64 tokens below the greatest
+    length it has had, or to any multiple of 64, from which that counts anew.
+
     ``buffers``: tensors of an earlier cache to take over, by the names
     ``k_codes``, ``v_codes`` [B, Hkv, capacity, d] (int8 or float8_e4m3fn),
     ``k_scales``, ``v_scales`` [B, Hkv, capacity / 64] (float32), ``k_recent``,

@@ -447,9 +447,15 @@ tq_status tq_export_vectors(tq_vec_index* index, const void* codes, int64_t star
  * length L, the tokens of its floor(L / 64) whole blocks are read from the
  * codes, and the L % 64 tokens of its open block from a 16-bit ring, where
  * position p has slot p % 128.  The ring also keeps the newest whole block's
- * tokens, so a row's length may be set back by up to 64 tokens of what was
- * appended last (rejected drafts): appending again from there gives the same
- * codes as if the rejected tokens had never been written.
+ * tokens, so a row's length may be set back (rejected drafts), and appending
+ * again from there gives the same codes as if the rejected tokens had never
+ * been written.  It may go back
+ *   - to 64 tokens below the greatest length that the row has had, however
+ *     many steps that takes and whatever is appended between them, or
+ *   - to any multiple of 64 (0 starts the row anew): from then on the greatest
+ *     length counts from there, and only another multiple of 64 lies below it.
+ * Beyond that the open block's tokens are no longer in the ring, which the
+ * calls do not notice.
  *
  * Quantisation of a block (64 x d values x, K and V apart), all in float32
  * with M = 127 (int8) or 448 (e4m3), each operation rounded to nearest even:

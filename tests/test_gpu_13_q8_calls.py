@@ -7,7 +7,7 @@ import torch
 
 from compressed_decode_attention_encode_b200 import tq
 from oracle import q8_oracle as O
-from tests.test_gpu_11_q8 import INT, Stream, rope_bound, values
+from tests.test_gpu_11_q8 import INT, Stream, rope_bound, run_attention, values
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +75,37 @@ def test_layers_share_a_streams_scratch():
             for j, st in enumerate(sts):
                 own = torch.empty(st.c.scratch_bytes(8, 1 + 2 * i), dtype=torch.uint8, device="cuda")
                 assert torch.equal(st.c.attention(q, lens[j], scratch=own), outs[20 * i + j])
+
+
+def assert_held(st):
+    """What is read back is the oracle's, bit for bit, of the tokens appended."""
+    b, h, d = st.shape
+    got = st.c.read(st.lens(), 0, max(st.len + [1]))
+    for w, x in zip("kv", got):
+        for i, n in enumerate(st.len):
+            for u in range(h):
+                codes, scales = O.held(st.x[w][i][u, :n].double().numpy(), n, st.fmt)
+                want = torch.from_numpy(codes.astype(np.float32) * scales.astype(np.float32)[:, None]).to(x.dtype)
+                assert torch.equal(x[i, u, :n].cpu(), want), (w, i, u)
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_rows_set_back_again_and_again(seed):
+    """Random appends and set-backs of three rows, within 64 tokens of the
+    greatest length since the last set-back to a multiple of 64, or to one."""
+    g = np.random.default_rng(seed)
+    st = Stream(3, 1, 64, 1024, "e4m3" if seed % 2 else "int8", "bf16" if seed % 2 else "fp16")
+    base, most = [0] * 3, [0] * 3
+    for step in range(25):
+        rows = [int(g.choice([0, 1, 5, 63, 64, 100, 150])) for _ in range(3)]
+        rows = [min(r, 1024 - n) for r, n in zip(rows, st.len)]
+        st.append(1000 * seed + step, max(rows + [1]), rows)
+        most = [max(m, n) for m, n in zip(most, st.len)]
+        assert_held(st)
+        run_attention(st, step, 2, 4)
+        for i in range(3):
+            if g.random() < 0.15:
+                base[i] = most[i] = st.len[i] = 64 * int(g.integers(0, st.len[i] // 64 + 1))
+            elif g.random() < 0.7:
+                st.len[i] = int(g.integers(min(st.len[i], max(base[i], most[i] - 64)), st.len[i] + 1))
+        run_attention(st, step, 2, 4)
