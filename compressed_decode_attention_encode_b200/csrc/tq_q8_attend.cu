@@ -92,12 +92,17 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)_
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
-// Result = numerator x this, with the numerator's reference gv (relative to the
-// denominator's).  A denominator of zero has no token behind it, or only logits
-// of -inf, which is no number.
-__device__ __forceinline__ float result_factor(float gv, float sum, bool sees) {
-  return sum == 0.f ? (sees ? NAN : 0.f) : ex2(gv) / sum;
-}
+// Result = numerator x both factors, with the numerator's reference gv (relative
+// to the denominator's), whose power of two alone may be no float32.  A
+// denominator of zero has no token behind it, or only logits of -inf, which is
+// no number.
+struct Factors {
+  float a, b;
+  __device__ __forceinline__ Factors(float gv, float sum, bool sees) {
+    a = ex2(0.5f * gv), b = sum == 0.f ? (sees ? NAN : 0.f) : a / sum;
+  }
+  __device__ __forceinline__ float operator()(float t) const { return t * a * b; }
+};
 template <typename T>
 __device__ __forceinline__ bool quad_bad(const uint4& v) {
   return pair_bad<T>(v.x) || pair_bad<T>(v.y) || pair_bad<T>(v.z) || pair_bad<T>(v.w);
@@ -757,8 +762,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q8_attend_kernel
       if (all) {
         const int i = (int)((uint32_t)(r0 + r) * ps.inv_g >> 16), h = kvh * a.G + (r0 + r) - i * a.G;
         T* out = static_cast<T*>(a.out) + (((size_t)row * a.n + i) * a.Hq + h) * D + d;
-        const float c = result_factor(gv, sum, ps.base + i > 0);
-        *reinterpret_cast<uint2*>(out) = make_uint2(pack16<T>(t.x * c, t.y * c), pack16<T>(t.z * c, t.w * c));
+        const Factors c(gv, sum, ps.base + i > 0);
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack16<T>(c(t.x), c(t.y)), pack16<T>(c(t.z), c(t.w)));
       } else {
         *reinterpret_cast<float4*>(part + r * S::OROW + d) = t;
         if (d == 0) *reinterpret_cast<float4*>(part + r * S::OROW + D) = make_float4(gl, gv, sum, 0.f);
@@ -855,9 +860,9 @@ __global__ void __launch_bounds__(kThreads) q8_join_kernel(const Q8AttendArgs a,
     }
   }
   if (WPR == 1) {
-    const float c = result_factor(gv, sum, sees);
+    const Factors c(gv, sum, sees);
 #pragma unroll
-    for (int e = 0; e < E; e += 2) reinterpret_cast<uint32_t*>(out)[(E * lane + e) / 2] = pack16<T>(o[e] * c, o[e + 1] * c);
+    for (int e = 0; e < E; e += 2) reinterpret_cast<uint32_t*>(out)[(E * lane + e) / 2] = pack16<T>(c(o[e]), c(o[e + 1]));
     return;
   }
   if (lane == 0) wm[warp][0] = gl, wm[warp][1] = gv, wm[warp][2] = sum;
@@ -877,7 +882,7 @@ __global__ void __launch_bounds__(kThreads) q8_join_kernel(const Q8AttendArgs a,
     sum += wm[w][2] * ex2(down);
     t += wo[w][threadIdx.x] * ex2(wm[w][1] + down - gv);
   }
-  out[threadIdx.x] = (T)(t * result_factor(gv, sum, sees));
+  out[threadIdx.x] = (T)Factors(gv, sum, sees)(t);
 }
 
 // A unit's query rows are cut into passes of up to 24, as even as eights allow.  24 rows are what registers

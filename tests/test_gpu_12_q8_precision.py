@@ -207,3 +207,20 @@ def test_a_flat_softmax_errs_by_its_own_rounding(fmt, d, n):
             err += ((got[i, :, 4 * u:4 * u + 4] - o) ** 2).sum()
             own += ((o.astype(np.float16) - o) ** 2).sum()
     assert err <= 1.1 ** 2 * own
+
+
+@pytest.mark.parametrize("length", [192, 8000])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_small_values_with_small_weights(fmt, length):
+    """Values of 2^-95 behind a block of zeros that takes all but 2^-29 of the
+    weight: the results are bf16 numbers, their factor alone no float32."""
+    st = Stream(2, 2, 64, 8000, fmt, "bf16")
+    k, v = values(15, (2, length, 2, 64), "bf16", False), values(16, (2, length, 2, 64), "bf16")
+    k[:, 64:128] = 11.0
+    v = (v.float() * 2.0 ** -95).bfloat16()
+    v[:, 64:128] = 0
+    st.append(0, length, k=k, v=v)
+    q = single(2, 1, 16, 64, "bf16", 16.0)
+    out = st.c.attention(q, st.lens())
+    assert out.any(-1).all()
+    assert_rounded(st, q, out)
