@@ -199,9 +199,10 @@ __global__ void __launch_bounds__(kReadThreads) q8_read_kernel(const Q8ReadArgs 
 // prompts: 12297 tokens of 40 heads of 128 (bf16) take 45 us, 5.6 TB/s; the
 // same with a head's halves loaded one head ahead into registers took 55.
 constexpr int kRopeThreads = 128, kRopeWarps = kRopeThreads / 32, kRopeAhead = 2;
+constexpr int kRopeCtas = 5;                               // per SM: 86 to 96 registers a thread
 
 template <typename T, int D, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads, 5) norm_rope_kernel(const NormRopeArgs a, int parts) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) norm_rope_kernel(const NormRopeArgs a, int parts) {
   constexpr int L = D / 16, HW = 32 / L;                   // lanes per head, heads per warp
   __shared__ float2 cs[kRopeWarps][D / 2];                 // a lane's i-th turn at [i L + lane]
   __shared__ uint4 buf[kRopeAhead * kRopeThreads * 2];     // [stage][warp][half][lane]
@@ -366,14 +367,10 @@ cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s) {
 }
 
 template <typename T, int D>
-static cudaError_t launch_rope(const NormRopeArgs& a, cudaStream_t s) {
+static cudaError_t launch_rope(const NormRopeArgs& a, int num_sms, cudaStream_t s) {
   const int64_t tokens = (int64_t)a.batch * a.n;
   const int passes = (a.Hq + a.Hkv + 32 / (D / 16) - 1) / (32 / (D / 16));
-  // A token's heads are split while there are fewer warps than the card holds (148 SMs x 24): a step's 8 tokens
-  // take 2.4 us so; whole tokens to a warp save the angles of the parts, 45 us against 48 for 12297 tokens in
-  // two parts.
-  const int64_t want = 148 * 24 / tokens;
-  const int parts = (int)(want < 1 ? 1 : want < passes ? want : passes);
+  const int parts = norm_rope_parts(tokens, passes, num_sms * kRopeCtas * kRopeWarps);
   const unsigned grid = (unsigned)((tokens * parts + kRopeWarps - 1) / kRopeWarps);
   cudaError_t e = cudaSuccess;
   auto go = [&](auto fn) { e = launch_dependent(fn, dim3(grid), kRopeThreads, 0, s, a, parts); };
@@ -382,9 +379,10 @@ static cudaError_t launch_rope(const NormRopeArgs& a, cudaStream_t s) {
   return e;
 }
 
-cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t s) {
-  if (a.dtype == TQ_DTYPE_FP16) return a.d == 64 ? launch_rope<__half, 64>(a, s) : launch_rope<__half, 128>(a, s);
-  return a.d == 64 ? launch_rope<__nv_bfloat16, 64>(a, s) : launch_rope<__nv_bfloat16, 128>(a, s);
+cudaError_t launch_norm_rope(const NormRopeArgs& a, int num_sms, cudaStream_t s) {
+  if (a.dtype == TQ_DTYPE_FP16)
+    return a.d == 64 ? launch_rope<__half, 64>(a, num_sms, s) : launch_rope<__half, 128>(a, num_sms, s);
+  return a.d == 64 ? launch_rope<__nv_bfloat16, 64>(a, num_sms, s) : launch_rope<__nv_bfloat16, 128>(a, num_sms, s);
 }
 
 }  // namespace tq

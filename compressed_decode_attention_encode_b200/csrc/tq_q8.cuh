@@ -66,6 +66,17 @@ struct NormRopeArgs {
   void* k_out;
 };
 
+// Parts that a token's heads (of so many passes) are split into, each a warp's:
+// while all of them fit on the card at once.  A step's 8 tokens of 40 heads of
+// 128 take 2.0 to 2.2 us so, 700 tokens 4.2 us in four parts (whole tokens to a
+// warp 6.0), 1184 tokens 5.1 in two (6.0); one part too many, which makes a
+// second, mostly empty wave, takes 1000 tokens from 5.1 to 6.6 us and 1776 from
+// 7.0 to 8.2.
+inline int norm_rope_parts(int64_t tokens, int passes, int warps) {
+  const int64_t fit = warps / tokens;
+  return (int)(fit < 1 ? 1 : fit < passes ? fit : passes);
+}
+
 // The kernel's arguments: what belongs to a side without heads is not used, so
 // nothing of it goes on.
 inline NormRopeArgs norm_rope_args(const tq_qk_norm_rope_args& x) {
@@ -82,7 +93,7 @@ cudaError_t launch_q8_append(const Q8AppendArgs& a, cudaStream_t s);
 cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s);
 size_t q8_attend_scratch(const tq_q8_cache& c, int Hq, int n, int num_sms);
 cudaError_t launch_q8_attend(const Q8AttendArgs& a, int num_sms, cudaStream_t s);
-cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t s);
+cudaError_t launch_norm_rope(const NormRopeArgs& a, int num_sms, cudaStream_t s);
 
 #ifdef __CUDACC__
 // Launches a kernel as a programmatic dependent of the stream's last one: its

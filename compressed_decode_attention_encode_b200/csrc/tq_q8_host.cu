@@ -138,7 +138,9 @@ tq_status tq_qk_norm_rope(const tq_qk_norm_rope_args* x, cudaStream_t stream) {
        !good_stride(x->k_row_stride) || !good_stride(x->k_token_stride) || !good_stride(x->k_head_stride)))
     return TQ_ERR_INVALID_ARG;
   const NormRopeArgs a = norm_rope_args(*x);
-  return launch_norm_rope(a, stream) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+  int sms;
+  if (sm_count(&sms) != cudaSuccess) return TQ_ERR_CUDA;
+  return launch_norm_rope(a, sms, stream) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -1,5 +1,7 @@
 // Host check of the norm and rotation's arguments: of a side without heads no
-// pointer or stride reaches the kernel, whatever the caller left there.
+// pointer or stride reaches the kernel, whatever the caller left there; and of
+// its split: the parts of all tokens fit on the card together, and one more of
+// each would not, unless a token has no more passes.
 #include <cstdio>
 #include <cstring>
 
@@ -23,6 +25,13 @@ int main() {
       bad += a.batch != 1 || a.n != 2 || a.Hq != hq || a.Hkv != hk || a.d != 128 || a.eps != 1e-6f || a.interleaved != 1 ||
              a.positions != x.positions || a.inv_freq != x.inv_freq;
     }
+  for (int warps : {20, 2960, 3000})
+    for (int passes : {1, 2, 3, 10, 16})
+      for (int64_t tokens : {1, 2, 8, 19, 20, 21, 185, 296, 700, 1000, 1479, 1480, 1481, 1776, 2960, 2961, 12297, 2147483647}) {
+        const int64_t parts = tq::norm_rope_parts(tokens, passes, warps);
+        bad += parts < 1 || parts > passes || (parts > 1 && tokens * parts > warps) ||
+               (parts < passes && tokens * (parts + 1) <= warps);
+      }
   std::printf(bad ? "bad %d\n" : "ok\n", bad);
   return bad != 0;
 }

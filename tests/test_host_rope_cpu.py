@@ -1,5 +1,5 @@
-"""The norm and rotation's arguments as the kernel gets them, compiled and run
-on the CPU (``tests/host/rope_args_check.cu``).  Needs nvcc only."""
+"""The norm and rotation's arguments as the kernel gets them, and its split of
+a token's heads, compiled and run on the CPU (``tests/host/rope_args_check.cu``).  Needs nvcc only."""
 import os
 import shutil
 import subprocess
