@@ -112,10 +112,12 @@ __device__ __forceinline__ bool quad_bad(const uint4& v) {
 __device__ __forceinline__ bool row_valid(const Q8AttendArgs& a, int len, int nr) {
   return len >= 0 && len <= a.c.capacity && nr >= 0 && nr <= a.n;
 }
-// What a unit costs besides its tiles, in tiles.  Measured: 33 ragged rows with one query each (NT = 1) take
-// 43.3 us with 8, 45.6 with 6, 51.8 with 4; 5 queries in each of 16 rows (NT = 3, heavier tiles) 28.4 with 8, 26.4
-// with 4, 27.4 with 3.
-constexpr int unit_cost(int nt) { return nt == 1 ? 8 : 4; }
+// What a unit costs besides its tiles, in tiles.  Measured, one query each (NT = 1) with 4, 6, 8 and 12: 33 ragged rows
+// up to 9001 tokens (bf16) 50.2, 45.1, 45.3 and 46.6 us; 64 up to 4000 46.1, 43.4, 46.1 and 49.1; 16 rows of 8192 with
+// 64 query heads 52.7, 53.0, 55.5 and 54.5; 16 rows of 4096 (fp16) 31.8, 32.8, 33.9 and 35.4.  5 queries in each of 16
+// ragged rows (NT = 3, heavier tiles) with 2, 3, 4 and 8: 33.0, 29.0, 27.9 and 30.4; 8 of them in rows of 4096 alike
+// with 2 to 4 (77.8), 81.3 with 8.
+constexpr int unit_cost(int nt) { return nt == 1 ? 6 : 4; }
 // In shared memory: places before each row [batch + 1], lengths [batch] (0 where a row has no work).
 struct Plan {
   uint32_t* pre;
