@@ -958,9 +958,9 @@ size_t q8_attend_scratch(const tq_q8_cache& c, int Hq, int n, int num_sms) {
 cudaError_t launch_q8_attend(const Q8AttendArgs& a, int num_sms, cudaStream_t s) {
   const uint32_t grid = grid_of(a.c, a.Hq, a.n, num_sms);
   // A call's two launches follow one another: between them another thread's call on the stream would overwrite
-  // the partial results, where both take the same scratch.
-  static std::mutex launches;
-  const std::lock_guard<std::mutex> hold(launches);
+  // the partial results, where both take the same scratch (others need not wait).
+  static std::mutex launches[64];
+  const std::lock_guard<std::mutex> hold(launches[(uintptr_t)a.scratch / 256 % 64]);
   const bool i8 = a.c.format == TQ_Q8_INT8;
   if (a.c.dtype == TQ_DTYPE_FP16)
     return i8 ? pick<__half, TQ_Q8_INT8>(a, grid, s) : pick<__half, TQ_Q8_E4M3>(a, grid, s);
