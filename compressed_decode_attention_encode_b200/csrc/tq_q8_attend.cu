@@ -11,9 +11,9 @@
 // and fp16 values are exact operands, sums and references float32.  Weights
 // enter the second product in parts that leave float32's own precision: two of
 // fp16 (2^-22), in a bf16 cache's open block three of bf16 (2^-24).  With one
-// fp16 part, which saved 0 to 5 %, the error beside an fp16 result's own
+// fp16 part, which saved up to 13 %, the error beside an fp16 result's own
 // rounding was 1.6 times as large where many tokens of either sign weigh
-// alike, and one bf16 result in twenty was rounded to the neighbour.
+// alike, and one bf16 result in a hundred was rounded to the neighbour.
 //
 // The work is the batch's tiles (a unit's whole blocks of 64 tokens, then its
 // open block), flattened and cut into equal runs, one per CTA, so that rows of
@@ -24,11 +24,14 @@
 // run is finished there; the others leave partial results that a second
 // kernel joins in a fixed order.
 //
-// One query per row is bound by HBM: 8 rows of 32768 tokens (32/8 heads of
-// 128, e4m3) take 90 to 95 us on the device, 5.7 to 6.0 TB/s, and the kernel
-// without its arithmetic as long.  Several queries are bound by the chain of
-// dependent instructions at 8 warps per SM: 5 queries in each of 16 ragged
-// rows up to 4109 tokens take 27 us where the bytes would take 8.
+// One query per row is bound by the fetch of the codes: 8 rows of 32768 tokens
+// (32/8 heads of 128, e4m3, fp16) take 90 us on the device, 6.0 TB/s, and the
+// kernel without its arithmetic as long (100 us in loops of a fifth of a second
+// and more, graphs and calls alike).  One row of 131583 (int8, bf16) takes 55.5
+// us, its fetch alone 49.4; 33 ragged rows (e4m3, bf16) 45.1 and 39.0.  Several
+// queries are bound by the chain of dependent instructions at 8 warps per SM: 5
+// in each of 16 ragged rows up to 4109 tokens take 27.9 us, the fetch alone
+// 15.5, where the bytes would take 7.6.
 #include <atomic>
 #include <cmath>
 #include <mutex>
@@ -39,8 +42,8 @@ namespace tq {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-// Stages of a warp's ring.  Two keep 48 KB per SM on their way, what HBM's latency asks for; with three, or with four
-// CTAs per SM, 8 rows of 32K tokens take 102 us instead of 94 (more outstanding reads make HBM slower).
+// Stages of a warp's ring.  Two keep 48 KB per SM on their way; with three 8 rows of 32K tokens take 99 us instead of
+// 90, 33 ragged rows 52 instead of 45, and 8 queries in 16 rows of 4096 76.5 instead of 77.8.
 constexpr int kStages = 2;
 constexpr float kLowest = -3.0e38f;          // ml before its first token
 constexpr float kShift = 7.f;                // numerator weights are 2^7 at their reference (dv holds it less 7),
@@ -169,7 +172,7 @@ __device__ __forceinline__ void plan_rows(const Q8AttendArgs& a, int subs, int c
   __syncthreads();
 }
 // A run has one place at least: with few, short rows the tiles' latency is what counts (a row of 1536 tokens with 4
-// kv heads: 6.7 us with one place a CTA, 7.3 with two, 8.3 with four).
+// kv heads: 6.4 us with one place a CTA; an earlier build 6.7, and 7.3 with two, 8.3 with four).
 __device__ __forceinline__ uint32_t plan_ctas(uint32_t places, uint32_t grid) { return places < grid ? places : grid; }
 // Runs of places / ctas places, one more in the first ones.
 struct Runs {
@@ -255,8 +258,9 @@ struct Shape {
   static_assert(NT <= kWarps);                             // a warp brings eight of them
   static constexpr int Q = QS ? NT * (D / 16) * 256 + ROWS * 4 : 0;
 };
-// CTAs per SM: what registers and shared memory allow (two queries' passes of d = 64 with three instead of two: 17.9
-// us instead of 19.1 for 8 rows of 8192).
+// CTAs per SM: what registers and shared memory allow, at spills of 40 bytes a thread at most (bf16, d = 128, NT = 1).
+// Two queries' passes of d = 64 with three instead of two: 19.5 us instead of 20.2 for 8 rows of 8192; NT = 1 of
+// d = 128 with four instead of three spills, 151 us instead of 90 for 8 rows of 32768.
 constexpr int ctas_per_sm(int d, int nt) { return nt == 1 ? (d == 128 ? 3 : 4) : nt == 2 && d == 64 ? 3 : 2; }
 template <int D, int NT>
 int smem_bytes(int batch) {
@@ -887,9 +891,10 @@ __global__ void __launch_bounds__(kThreads) q8_join_kernel(const Q8AttendArgs a,
   out[threadIdx.x] = (T)Factors(gv, sum, sees)(t);
 }
 
-// A unit's query rows are cut into passes of up to 24, as even as eights allow.  24 rows are what registers
-// hold: a pass of 32 spilled, and took 81 us (int8, fp16) and 123 us (e4m3, bf16) for 8 queries of 4 heads over 16
-// rows of 4096 tokens (8 kv heads of 128), where two passes of 16 took 78 and 75.
+// A unit's query rows are cut into passes of up to 24, as even as eights allow.  24 rows are what the registers hold
+// (251 to 255 of them, up to 28 bytes spilled for bf16 of d = 128); passes of up to 32 spill more.  16 rows of 4096
+// tokens (32 / 8 heads of 128): 8 queries take 77.8 us (int8, fp16) and 70.0 (e4m3, bf16) so, 80.1 and 112 with 32 rows;
+// 64 queries 456 us, 521 with 32 and 553 with 16.
 int pick_nt(int rows) {
   const int eights = (rows + 7) / 8, passes = (eights + 2) / 3;
   return (eights + passes - 1) / passes;
@@ -923,8 +928,9 @@ cudaError_t launch(const Q8AttendArgs& a, uint32_t grid, cudaStream_t s) {
   }
   e = launch_dependent(kernel, dim3(grid), kThreads, smem_bytes<D, NT>(a.c.batch), s, a);
   if (e != cudaSuccess) return e;
-  // A warp per query row where units have some 16 partial results at most: 8 queries of 4 heads in 16 rows of 4096
-  // take 69 us so, 78 with four warps a row.  Else four: a row of 131583 tokens takes 53.3 us so, 57.0 with one.
+  // A warp per query row where units have some 16 partial results at most, else four.  One and four warps: 5 queries in
+  // 16 ragged rows 27.9 and 32.1 us, 256 rows of 512 tokens 67.7 and 80.0, 16 rows of 4096 33.8 and 34.3; 4 rows of 8192
+  // 21.8 and 21.5; one row of 8192 14.9 and 11.6, of 131583 59.5 and 55.9.
   const int rows = a.c.num_kv_heads * a.n * a.G, units = a.c.batch * a.c.num_kv_heads * groups_of(a.c, a.Hq, a.n);
   const int join_smem = 4 * (2 * a.c.batch + 1);
   if ((int64_t)units * 16 >= grid)
