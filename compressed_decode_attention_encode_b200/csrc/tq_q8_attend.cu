@@ -464,6 +464,7 @@ struct Pass {
     float s[NT][4], f[NT][2], lsv = 0.f;
     uint32_t bad = 0;                                      // the open block's tokens with a NaN or an infinity
     uint4 vo[4][KS / 4];                                   // its values
+    float up = 1.f;                                        // bf16: what its weights are short of
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -539,6 +540,24 @@ struct Pass {
             mma16816(s[t], k[0].z, k[1].z, k[0].w, k[1].w, b1.x, b1.y, T());
           }
         }
+      if (Pair16<T>::kWide) {
+        // The open block's values stand for themselves, at a scale of 1; bf16 ones may be so small, or zeros, that the
+        // reference of that scale would leave what the whole blocks gave below float32.  So the reference takes the
+        // power of two of the largest, and the weights that power back.
+        __nv_bfloat162 m2 = __floats2bfloat162_rn(0.f, 0.f);  // NaN drops out; infinities count as 1 and more
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int x = 0; x < KS; ++x) {
+            const uint32_t v = word(vo[i][x / 4], x % 4);
+            m2 = __hmax2(m2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v)));
+          }
+        uint32_t mx = *reinterpret_cast<const uint32_t*>(&m2);
+        mx = __reduce_max_sync(~0u, max(mx & 0xffffu, mx >> 16));
+        const int k = min(max(127 - (int)(mx >> 7), 0), 100);   // 0 for values of 1 and more
+        lsv = mx == 0 ? kNothing : (float)-k;
+        up = __uint_as_float((uint32_t)(127 + k) << 23);
+      }
     }
     weights(s, f, lsv, first, open || (tile + 1) * kQ8Block > base + (int)((uint32_t)r0 * inv_g >> 16));
     if (!open) {
@@ -587,6 +606,11 @@ struct Pass {
           for (int e = 0; e < 4; ++e)
             if ((bad >> (gid + 8 * (e >> 1)) & 1) && first + gid + 8 * (e >> 1) < end_of(t, e & 1)) s[t][e] = NAN;
       }
+      if (Pair16<T>::kWide)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[t][e] *= up;
 #pragma unroll
       for (int part = 0; part < OPEN_PARTS; ++part) {
         uint32_t b[NT][2];

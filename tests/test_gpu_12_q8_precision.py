@@ -224,3 +224,24 @@ def test_small_values_with_small_weights(fmt, length):
     out = st.c.attention(q, st.lens())
     assert out.any(-1).all()
     assert_rounded(st, q, out)
+
+
+@pytest.mark.parametrize("d,n", [(64, 1), (128, 3)])
+@pytest.mark.parametrize("last", ["zeros", "one element", "small"])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_the_open_block_of_small_values_takes_the_weight(fmt, last, d, n):
+    """Whole blocks of values of 2^-95 with 2^-33 of the weight; the rest lies on
+    the open block, whose values are zeros, zeros but for one element of its
+    tokens, or as small."""
+    st = Stream(2, 2, d, 256, fmt, "bf16")
+    k, v = values(17, (2, 250, 2, d), "bf16", False), (values(18, (2, 250, 2, d), "bf16").float() * 2.0 ** -95).bfloat16()
+    k[:, 192:] = 11.5
+    if last == "zeros":
+        v[:, 192:] = 0
+    if last == "one element":
+        v[:, 192:, :, 1:] = 0
+    st.append(0, 250, k=k, v=v)
+    q = single(2, n, 16, d, "bf16", 2 * math.sqrt(d))
+    out = st.c.attention(q, st.lens())
+    assert out.any(-1).all()
+    assert_rounded(st, q, out)
