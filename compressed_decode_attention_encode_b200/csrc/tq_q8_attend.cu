@@ -27,8 +27,8 @@
 // One query per row is bound by the fetch of the codes: 8 rows of 32768 tokens
 // (32/8 heads of 128, e4m3, fp16) take 90 us on the device, 6.0 TB/s, and the
 // kernel without its arithmetic as long (100 us in loops of a fifth of a second
-// and more, graphs and calls alike).  One row of 131583 (int8, bf16) takes 55.5
-// us, its fetch alone 49.4; 33 ragged rows (e4m3, bf16) 45.1 and 39.0.  Several
+// and more, graphs and calls alike).  One row of 131583 (int8, bf16) takes 56.2
+// us, its fetch alone 49.4; 33 ragged rows (e4m3, bf16) 45.5 and 39.0.  Several
 // queries are bound by the chain of dependent instructions at 8 warps per SM: 5
 // in each of 16 ragged rows up to 4109 tokens take 27.9 us, the fetch alone
 // 15.5, where the bytes would take 7.6.
