@@ -543,8 +543,8 @@ tq_status tq_q8_attention_bytes(const tq_q8_cache* cache, int32_t num_q_heads, i
  *   softmax_scale  sigma; 0 selects 1/sqrt(d)
  *   scratch  device, 256-byte aligned, at least tq_q8_attention_bytes; it
  *            holds nothing between calls, and calls whose GPU work overlaps
- *            need one each (calls on one stream do not overlap, whatever host
- *            threads they come from)
+ *            need one each (calls on one stream with the same scratch do not
+ *            overlap, whatever host threads they come from)
  * Query i of row b attends to its positions below lens[b] - n_rows[b] + 1 + i:
  *   out = sum_p softmax_p(sigma <q, k_p>) v_p
  * and is zero where there is none.  Sums and softmax statistics are float32;
